@@ -15,7 +15,8 @@ from typing import Optional
 import numpy as np
 
 __all__ = ["ClError", "lib", "pack", "blob_header", "CompressedLinear", "fit_lut", "fit_int", "quant_absmax", "LIB_PATH",
-           "EXPORTED_SYMBOLS", "PROBE_SYMBOLS"]
+           "EXPORTED_SYMBOLS", "PROBE_SYMBOLS", "SERVING_SYMBOLS", "rope_table", "rope", "KVCache", "tree_attention",
+           "token_logprobs"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcompressed_linear.so")
 
@@ -27,6 +28,10 @@ EXPORTED_SYMBOLS = [
 
 # measurement aids of the benchmark (include/cl_probe.h), exported by the same library
 PROBE_SYMBOLS = ["cl_probe_read", "cl_probe_read_sink_words", "cl_probe_empty"]
+
+# the operators around the layers (include/cl_serving.h), exported by the same library
+from .serving import (SERVING_SYMBOLS, KVCache, cl_kv_cache, declare as _declare_serving, rope, rope_table,  # noqa: E402
+                      token_logprobs, tree_attention)
 
 DENSE = {"lut3": 0, "lut4": 1, "int4": 2, "int8": 3}
 MASK = {"none": 0, "2:4": 1, "bitmap": 2}
@@ -136,6 +141,7 @@ def lib():
         L.cl_probe_read_sink_words.restype = ctypes.c_size_t
         L.cl_probe_empty.argtypes = [ctypes.c_void_p]
         L.cl_probe_empty.restype = ctypes.c_int
+        _declare_serving(L)
         _lib = L
     return _lib
 

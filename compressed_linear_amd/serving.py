@@ -1,0 +1,308 @@
+"""Python binding of the operators around the compressed linear layers
+(include/cl_serving.h): rotary positions, the quantised K/V cache, attention of
+drafted tokens over it, and log probabilities of given tokens.
+
+Argument checks and marshalling only; every step runs in the HIP library, on
+torch's current stream of the tensors' device.  Index tensors are int32.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+SERVING_SYMBOLS = ["cl_rope_table", "cl_rope", "cl_kv_append", "cl_kv_read", "cl_tree_attention_work_bytes",
+                   "cl_tree_attention", "cl_token_logprobs_work_bytes", "cl_token_logprobs"]
+
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+KV_KIND = {"int8": 0, "int4": 1}
+
+
+class cl_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+def declare(L):
+    """Argument types of the entry points, on the loaded library."""
+    p, i, q, d = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+    cache = ctypes.POINTER(cl_kv_cache)
+    L.cl_rope_table.argtypes = [i, i, d, i, d, i, d, d, p, p]
+    L.cl_rope.argtypes = [p, i, q, q, i, i, i, p, p, i, i, i, p, i, q, q, p]
+    L.cl_kv_append.argtypes = [cache, p, p, i, i, q, q, q, q, p, p, p, i, i, i, p]
+    L.cl_kv_read.argtypes = [cache, p, i, p, p, i, p]
+    L.cl_tree_attention_work_bytes.argtypes = [i] * 6
+    L.cl_tree_attention.argtypes = [p, i, q, q, i, i, cache, p, i, i, p, p, i, i, p, i, ctypes.c_float, p, p,
+                                    ctypes.c_size_t, p]
+    L.cl_token_logprobs_work_bytes.argtypes = [i] * 3
+    L.cl_token_logprobs.argtypes = [p, i, q, i, i, p, i, p, p, i, p, p, p, ctypes.c_size_t, p]
+    for name in SERVING_SYMBOLS:
+        getattr(L, name).restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
+
+
+_torch = None
+_lib = None
+_DT: dict = {}
+
+
+def _setup():
+    """torch and the library, loaded at the first call (importing the package needs neither)."""
+    global _torch, _lib
+    if _lib is None:
+        import torch
+
+        from . import lib
+        _lib = lib()
+        _DT.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+        _torch = torch
+    return _lib
+
+
+def _check(st: int, where: str):
+    if st != 0:
+        from . import _check as check
+        check(st, where)
+
+
+def _stream(dev):
+    """torch's current stream on `dev`; the library launches on the current device, so that has to be it."""
+    if dev.index != _torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{_torch.cuda.current_device()}")
+    return _torch.cuda.current_stream(dev).cuda_stream
+
+
+def _index(t, n, dev, what):
+    """The address of an int32 tensor of n elements on `dev`."""
+    if t.dtype != _torch.int32 or t.device != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of {n} elements on {dev}")
+    return t.data_ptr()
+
+
+def _heads3(x, what):
+    """A [tokens, heads, dim] tensor of 16 or 32 bits with contiguous channels (copied if they are not)."""
+    if x.dim() != 3 or x.dtype not in _DT or not x.is_cuda:
+        raise ValueError(f"{what} must be a float16, bfloat16 or float32 [tokens, heads, dim] tensor on a ROCm device")
+    return x if x.stride(2) == 1 else x.contiguous()
+
+
+def _table(table, dev):
+    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != _torch.float32 or table.device != dev \
+            or not table.is_contiguous():
+        raise ValueError(f"table must be a contiguous float32 [positions, rot / 2, 2] tensor on {dev} (see rope_table)")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               trained: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Cosines and sines of `positions` positions for a rotation over `rot` channels (cl_rope_table): a
+    float32 tensor [positions, rot / 2, 2].  scaling 'none', 'linear', 'ntk' or 'yarn' (by `factor`;
+    'yarn' also reads `trained`, `beta_fast` and `beta_slow`)."""
+    L = _setup()
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALING)}")
+    dev = _torch.device("cuda", _torch.cuda.current_device()) if device is None else _torch.device(device)
+    if positions < 1 or rot < 2 or rot % 2:
+        raise ValueError("positions >= 1 and an even rot >= 2 are wanted")
+    out = _torch.empty((positions, rot // 2, 2), dtype=_torch.float32, device=dev)
+    _check(L.cl_rope_table(positions, rot, base, ROPE_SCALING[scaling], factor, trained, beta_fast, beta_slow,
+                           out.data_ptr(), _stream(out.device)), "cl_rope_table")
+    return out
+
+
+def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None):
+    """Rotary positions (cl_rope): x [tokens, heads, dim] float16, bfloat16 or float32 (any token and head
+    strides, so a view of a qkv output will do), positions int32 [tokens], table from `rope_table`; the
+    first 2 * table.shape[1] channels are rotated, the others copied.  Returns `out`, or a new
+    contiguous tensor of `out_dtype` (x's type by default).  `out` may be x."""
+    L = _lib or _setup()
+    x = _heads3(x, "x")
+    dev = x.device
+    T, H, D = x.shape
+    if out is None:
+        out = _torch.empty((T, H, D), dtype=out_dtype or x.dtype, device=dev)
+    elif out.shape != x.shape or out.device != dev or out.stride(2) != 1 or (out_dtype or out.dtype) != out.dtype:
+        raise ValueError(f"out must be a {tuple(x.shape)} tensor on {dev} with contiguous channels")
+    if out.dtype not in _DT:
+        raise ValueError("the output must be float16, bfloat16 or float32")
+    tp, rows, rot = _table(table, dev)
+    st = L.cl_rope(x.data_ptr(), _DT[x.dtype], x.stride(0), x.stride(1), T, H, D,
+                   _index(positions, T, dev, "positions"), tp, rows, rot, ROPE_LAYOUT[layout], out.data_ptr(),
+                   _DT[out.dtype], out.stride(0), out.stride(1), _stream(dev))
+    _check(st, "cl_rope")
+    return out
+
+
+class KVCache:
+    """A paged, quantised K/V cache on one GPU (cl_kv_cache): kind 'int8' (a scale to each token and head)
+    or 'int4' (a scale to each 32 channels).  Slot s is place s % page_size of page s // page_size.
+
+    Either sizes are given and the cache allocates its tensors, or the four tensors are:
+    k, v uint8 [pages, heads, page_size, dim or dim / 2]; k_scale, v_scale float16 [pages, heads,
+    page_size] or [pages, heads, page_size, dim / 32].  It also keeps the attention's workspace: one
+    `tree_attention` at a time per cache.
+    """
+
+    def __init__(self, pages: int = 0, page_size: int = 64, heads: int = 1, dim: int = 128, kind: str = "int8",
+                 device=None, k=None, v=None, k_scale=None, v_scale=None):
+        _setup()
+        torch = _torch
+        if kind not in KV_KIND:
+            raise ValueError(f"kind must be one of {list(KV_KIND)}")
+        four = (k, v, k_scale, v_scale)
+        if all(t is None for t in four):
+            dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+            width = dim if kind == "int8" else dim // 2
+            tail = () if kind == "int8" else (dim // 32,)
+            k, v = (torch.zeros((pages, heads, page_size, width), dtype=torch.uint8, device=dev) for _ in range(2))
+            k_scale, v_scale = (torch.zeros((pages, heads, page_size) + tail, dtype=torch.float16, device=dev)
+                                for _ in range(2))
+        elif any(t is None for t in four):
+            raise ValueError("k, v, k_scale and v_scale are given together")
+        if k.dim() != 4:
+            raise ValueError("k must be uint8 [pages, heads, page_size, dim or dim / 2]")
+        pages, heads, page_size, width = k.shape
+        dim = width if kind == "int8" else 2 * width
+        tail = () if kind == "int8" else (dim // 32,)
+        for t, shape, dt in ((k, k.shape, torch.uint8), (v, k.shape, torch.uint8),
+                             (k_scale, (pages, heads, page_size) + tail, torch.float16),
+                             (v_scale, (pages, heads, page_size) + tail, torch.float16)):
+            if tuple(t.shape) != tuple(shape) or t.dtype != dt or t.device != k.device or not t.is_cuda \
+                    or not t.is_contiguous():
+                raise ValueError(f"a cache tensor must be a contiguous {dt} tensor {tuple(shape)} on one ROCm device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kind, self.pages, self.page_size, self.heads, self.dim = kind, pages, page_size, heads, dim
+        self.device = k.device
+        self._desc = cl_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page_size,
+                                 heads, dim, KV_KIND[kind], 0)
+        self._ref = ctypes.byref(self._desc)
+        self._work = None
+        self._outgrown: list = []
+
+    def append(self, k, v, slots, positions=None, table=None, layout: str = "half"):
+        """Quantise new keys and values [tokens, heads, dim] into `slots` (int32 [tokens]; a slot outside the
+        cache, -1 say, stores nothing).  With `table` (and int32 `positions`) the keys are rotated on
+        the way, from unrounded results, as `rope` would."""
+        k, v, dev = _heads3(k, "k"), _heads3(v, "v"), self.device
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != dev or v.device != dev \
+                or k.shape[1] != self.heads or k.shape[2] != self.dim:
+            raise ValueError(f"k and v must be [tokens, {self.heads}, {self.dim}] of one type on {dev}")
+        T = k.shape[0]
+        pp = tp = None
+        rows = rot = 0
+        if table is not None:
+            tp, rows, rot = _table(table, dev)
+            if positions is None:
+                raise ValueError("a table needs positions")
+            pp = _index(positions, T, dev, "positions")
+        st = _lib.cl_kv_append(self._ref, k.data_ptr(), v.data_ptr(), _DT[k.dtype], T, k.stride(0), k.stride(1),
+                               v.stride(0), v.stride(1), _index(slots, T, dev, "slots"), pp, tp, rows, rot,
+                               ROPE_LAYOUT[layout], _stream(dev))
+        _check(st, "cl_kv_append")
+
+    def read(self, slots, dtype=None):
+        """The stored keys and values of `slots` (int32 [n]): two tensors [n, heads, dim] of `dtype` (float16
+        by default), zeros for a slot outside the cache."""
+        dev = self.device
+        dtype = dtype or _torch.float16
+        if dtype not in _DT:
+            raise ValueError("dtype must be float16, bfloat16 or float32")
+        n = slots.numel()
+        k = _torch.empty((n, self.heads, self.dim), dtype=dtype, device=dev)
+        v = _torch.empty((n, self.heads, self.dim), dtype=dtype, device=dev)
+        st = _lib.cl_kv_read(self._ref, _index(slots, n, dev, "slots"), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
+                             _stream(dev))
+        _check(st, "cl_kv_read")
+        return k, v
+
+    def _workspace(self, sizes):
+        """The workspace for these sizes, zeroed when it is made (the calls leave it zeroed).  One that was
+        outgrown is kept: work on another stream or a recorded graph may still use it."""
+        need = _lib.cl_tree_attention_work_bytes(*sizes)
+        if need and (self._work is None or self._work.numel() < need):
+            if self._work is not None:
+                self._outgrown.append(self._work)
+            self._work = _torch.zeros(2 * need, dtype=_torch.uint8, device=self.device)
+        return self._work
+
+
+def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, max_ctx: Optional[int] = None,
+                   tree_mask=None, scale: Optional[float] = None, out=None):
+    """Attention of each sequence's newest tokens over its cached keys and values (cl_tree_attention).
+
+    q [tokens, q_heads, dim] float16 or bfloat16: the new tokens of all sequences, those of sequence b in
+    rows cu_q[b] .. cu_q[b + 1] (int32 [sequences + 1]); they are already in the cache, after its
+    ctx_lens[b] (int32 [sequences]) older tokens.  block_table int32 [sequences, width] names the
+    cache pages.  tree_mask int64 [tokens, words]: bit i of a row is set where the row's token sees
+    new token i of its sequence (None: the tokens form a chain).  max_q is at least every sequence's number
+    of new tokens (at most 256); max_ctx the longest context, which sizes the launch (default: what the
+    block table holds).  Returns [tokens, q_heads, dim] of q's type."""
+    L = _lib or _setup()
+    dev = cache.device
+    if q.dim() != 3 or q.device != dev or q.shape[2] != cache.dim or _DT.get(q.dtype, 2) == 2:
+        raise ValueError(f"q must be a float16 or bfloat16 [tokens, q_heads, {cache.dim}] tensor on {dev}")
+    if q.stride(2) != 1 or q.stride(0) % 8 or q.stride(1) % 8 or q.data_ptr() % 16:
+        q = q.contiguous()
+    T, H, D = q.shape
+    B = ctx_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be int32 [{B}, width]")
+    width = block_table.shape[1]
+    words, mp = 0, None
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.dtype != _torch.int64 or tree_mask.device != dev \
+                or tree_mask.shape[0] != T or not tree_mask.is_contiguous():
+            raise ValueError(f"tree_mask must be a contiguous int64 [{T}, words] tensor on {dev}")
+        words, mp = tree_mask.shape[1], tree_mask.data_ptr()
+    if out is None:
+        out = _torch.empty((T, H, D), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and type")
+    if max_ctx is None:
+        max_ctx = width * cache.page_size
+    args = (q.data_ptr(), _DT[q.dtype], q.stride(0), q.stride(1), T, H, cache._ref,
+            _index(block_table, B * width, dev, "block_table"), width, B, _index(ctx_lens, B, dev, "ctx_lens"),
+            _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
+            1.0 / D ** 0.5 if scale is None else scale, out.data_ptr())
+    work = cache._work
+    st = L.cl_tree_attention(*args, None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
+                             _stream(dev))
+    if st == -3:  # the workspace is too small for these sizes: make a larger one, once
+        work = cache._workspace((B, H, cache.heads, D, max_q, max_ctx))
+        st = L.cl_tree_attention(*args, work.data_ptr(), work.numel(), _stream(dev))
+    _check(st, "cl_tree_attention")
+    return out
+
+
+def token_logprobs(logits, ids, top_k: int = 0):
+    """Log probabilities of given tokens (cl_token_logprobs): logits [rows, vocab] float16, bfloat16 or float32,
+    ids int32 [rows, given].  Returns (logp float32 [rows, given], entropy float32 [rows]) and, with top_k > 0
+    (at most 32), top_ids int32 [rows, top_k] and top_logp float32 [rows, top_k]: the largest logits first,
+    equal ones by the lower id.  An id outside the vocabulary gives NaN."""
+    L = _lib or _setup()
+    if logits.dim() != 2 or logits.dtype not in _DT or not logits.is_cuda:
+        raise ValueError("logits must be a float16, bfloat16 or float32 [rows, vocab] tensor on a ROCm device")
+    if logits.stride(1) != 1:
+        logits = logits.contiguous()
+    dev = logits.device
+    T, V = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids must be int32 [{T}, given]")
+    C = ids.shape[1]
+    ip = _index(ids, T * C, dev, "ids")
+    # one allocation holds the float outputs
+    buf = _torch.empty(T * (C + 1 + top_k), dtype=_torch.float32, device=dev)
+    logp, entropy = buf[:T * C].view(T, C), buf[T * C:T * (C + 1)]
+    top_ids = top_logp = None
+    if top_k:
+        top_ids = _torch.empty((T, top_k), dtype=_torch.int32, device=dev)
+        top_logp = buf[T * (C + 1):].view(T, top_k)
+    need = L.cl_token_logprobs_work_bytes(T, V, top_k)
+    work = _torch.empty(need, dtype=_torch.uint8, device=dev) if need else None
+    st = L.cl_token_logprobs(logits.data_ptr(), _DT[logits.dtype], logits.stride(0), T, V, ip, C, logp.data_ptr(),
+                             entropy.data_ptr(), top_k, None if top_ids is None else top_ids.data_ptr(),
+                             None if top_logp is None else top_logp.data_ptr(),
+                             None if work is None else work.data_ptr(), need, _stream(dev))
+    _check(st, "cl_token_logprobs")
+    return (logp, entropy, top_ids, top_logp) if top_k else (logp, entropy)
