@@ -23,8 +23,8 @@
 // wavefront a step), so that the output is rarely rescaled.
 //
 // The keys of a sequence are cut into chunks, a workgroup each, whose four
-// wavefronts take every fourth block of 32 keys; partial outputs of more than one
-// chunk are joined, in chunk order, by the workgroup that finishes last.
+// wavefronts take every fourth block of 32 keys; the partial outputs of more than one
+// chunk are joined by a second, small launch.
 #include "serving.h"
 #include "unpack.h"
 
@@ -43,9 +43,7 @@ constexpr float kNone = -3.4e38f;  // running maximum before any key
 constexpr float kSlack = 4.f;      // log2 by which a score may pass the running maximum
 constexpr int kProbBits = 11;      // probabilities are scaled by 2^11: with the slack at most 2^15
 
-// Cells (sequence, kv head, row group) whose keys may be cut into chunks; their counters open the workspace, at
-// places that do not move with the sizes of a call.
-constexpr int kMaxCells = 4096;
+constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
 
 struct AttnArgs {
   const uint16_t* q;
@@ -55,18 +53,42 @@ struct AttnArgs {
   const int32_t* ctx_lens;
   const int32_t* cu_q;
   const uint64_t* mask;
-  uint32_t* counters;
   float2* part_ml;
   float* part_o;
   int64_t q_token, q_head;
   int tokens, group, table_width, max_q, mask_words, bf16;
-  int chunk, row_groups, page_shift;
+  int chunk, row_groups, rows_per_group, page_shift;
   float scale;
 };
 
 __device__ __forceinline__ f4 mfma16(const uint32_t (&a)[4], const uint32_t (&b)[4], f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, u4{a[0], a[1], a[2], a[3]}),
                                                 __builtin_bit_cast(h8, u4{b[0], b[1], b[2], b[3]}), c, 0, 0, 0);
+}
+
+// Two outputs in one word.
+__device__ __forceinline__ uint32_t pack16(int bf16, float x, float y) {
+  return bf16 ? Elem<CL_BF16>::down(x) | (uint32_t)Elem<CL_BF16>::down(y) << 16
+              : Elem<CL_F16>::down(x) | (uint32_t)Elem<CL_F16>::down(y) << 16;
+}
+
+// A sequence's rows and keys, and how its keys are cut: `splits` chunks of at least a.chunk keys, at most
+// `max_splits` (a sequence longer than the launch was sized for gets longer chunks).
+struct Range {
+  int first, n_new, ctx, splits;
+  int64_t n, chunk;
+};
+__device__ __forceinline__ Range range_of(const AttnArgs& a, int b, int max_splits) {
+  Range x;
+  x.first = a.cu_q[b];
+  const int64_t n_new = (int64_t)a.cu_q[b + 1] - x.first;
+  x.n_new = x.first < 0 || n_new < 0 || n_new > a.max_q || x.first + n_new > a.tokens ? 0 : (int)n_new;
+  x.ctx = max(a.ctx_lens[b], 0);
+  x.n = (int64_t)x.ctx + x.n_new;
+  const int64_t least = (x.n + max_splits - 1) / max_splits;
+  x.chunk = least <= a.chunk ? a.chunk : (least + kBlock * kWaves - 1) / (kBlock * kWaves) * (kBlock * kWaves);
+  x.splits = (int)((x.n + x.chunk - 1) / x.chunk);
+  return x;
 }
 
 // Largest value of the four lanes that hold parts of one row (16 apart).
@@ -124,21 +146,14 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
   constexpr int ROWS = 16 * RT, STRIDE = D + 4;
   __shared__ __align__(16) float s_o[kWaves][ROWS][STRIDE];
   __shared__ float2 s_ml[kWaves][ROWS];
-  __shared__ int s_last;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, c16 = l & 15, g = l >> 4;
   const int b = blockIdx.z, hk = blockIdx.y % a.c.heads, rg = blockIdx.y / a.c.heads;
-  const int first = a.cu_q[b], n_new = a.cu_q[b + 1] - first;
-  if (first < 0 || n_new <= 0 || n_new > a.max_q || first + n_new > a.tokens) return;
+  const Range range = range_of(a, b, gridDim.x);
+  const int first = range.first, n_new = range.n_new, ctx = range.ctx, splits = range.splits, split = blockIdx.x;
+  const int64_t n = range.n, chunk = range.chunk;
   const int G = a.group, rows = min(n_new * G - rg * ROWS, ROWS);  // rows of this workgroup that exist
-  if (rows <= 0) return;
-  const int ctx = max(a.ctx_lens[b], 0);
-  const int64_t n = (int64_t)ctx + n_new;
-  // a longer sequence than the launch was sized for makes the chunks longer
-  const int64_t least = (n + gridDim.x - 1) / gridDim.x;
-  const int64_t chunk = least <= a.chunk ? a.chunk : (least + kBlock * kWaves - 1) / (kBlock * kWaves) * (kBlock * kWaves);
-  const int splits = (int)((n + chunk - 1) / chunk), split = blockIdx.x;
-  if (split >= splits) return;
+  if (rows <= 0 || split >= splits) return;
   const int64_t k0 = split * chunk;
   const int blocks = (int)((min(n, k0 + chunk) - k0 + kBlock - 1) / kBlock);
 
@@ -458,11 +473,7 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
     const int at = rg * ROWS + row;
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x0 = x[2 * j] * inv, x1 = x[2 * j + 1] * inv;
-      w[j] = a.bf16 ? Elem<CL_BF16>::down(x0) | (uint32_t)Elem<CL_BF16>::down(x1) << 16
-                    : Elem<CL_F16>::down(x0) | (uint32_t)Elem<CL_F16>::down(x1) << 16;
-    }
+    for (int j = 0; j < 4; ++j) w[j] = pack16(a.bf16, x[2 * j] * inv, x[2 * j + 1] * inv);
     uint16_t* op = a.o + ((int64_t)(first + at / G) * (a.c.heads * G) + hk * G + at % G) * D + ch;
     *reinterpret_cast<u4*>(op) = u4{w[0], w[1], w[2], w[3]};
   };
@@ -481,39 +492,67 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
       store(row, x, den == 0.f ? 0.f : 1.f / den);
     } else {
       const int64_t at = (cell * gridDim.x + split) * ROWS + row;
-      if (ch == 0) {
-        store_dev(&a.part_ml[at].x, top);
-        store_dev(&a.part_ml[at].y, den);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) store_dev(&a.part_o[at * D + ch + j], x[j]);
+      if (ch == 0) a.part_ml[at] = make_float2(top, den);
+      f4* po = reinterpret_cast<f4*>(a.part_o + at * D + ch);
+      po[0] = f4{x[0], x[1], x[2], x[3]};
+      po[1] = f4{x[4], x[5], x[6], x[7]};
     }
   }
-  if (splits == 1) return;
-  // ---- join the chunks: the workgroup that comes last
-  wait_stores();
+}
+
+// Joins the partial outputs of a row's chunks, in chunk order within each of eight strands and the strands in
+// order: 32 lanes (dim 128) or 16 hold four channels each.  A launch of its own rather than the workgroup that
+// finishes last: rows x chunks partials are read by as many workgroups as there are rows.
+template <int D>
+__global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, int max_splits) {
+  constexpr int LANES = D / 4, STRANDS = 256 / LANES;
+  __shared__ float s_w[kMaxSplits];
+  __shared__ __align__(16) f4 s_x[STRANDS][LANES];
+  __shared__ float s_red[2 * kWaves];
+  const int tid = threadIdx.x, cell = blockIdx.x, row = blockIdx.y;
+  const int rg = cell % a.row_groups, hk = cell / a.row_groups % a.c.heads, b = cell / a.row_groups / a.c.heads;
+  const Range x = range_of(a, b, max_splits);
+  const int G = a.group, at = rg * a.rows_per_group + row;
+  if (x.splits < 2 || at >= x.n_new * G) return;
+  const int64_t base = (int64_t)cell * max_splits * a.rows_per_group + row;
+  const int ch = tid % LANES, strand = tid / LANES;
+  float top = kNone;
+  for (int v = tid; v < x.splits; v += 256) top = fmaxf(top, a.part_ml[base + (int64_t)v * a.rows_per_group].x);
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (tid % 64 == 0) s_red[tid / 64] = top;
   __syncthreads();
-  if (tid == 0) {
-    const uint32_t before = __hip_atomic_fetch_add(&a.counters[cell], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = before == (uint32_t)splits - 1;
-    if (s_last) __hip_atomic_store(&a.counters[cell], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!s_last) return;
-  for (int row = tid / PARTS; row < rows; row += 256 / PARTS) {
-    const int64_t base = cell * gridDim.x * ROWS + row;
-    float top = kNone, den = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int v = 0; v < splits; ++v) {
-      const int64_t at = base + (int64_t)v * ROWS;
-      const float mv = load_dev(&a.part_ml[at].x), lv = load_dev(&a.part_ml[at].y);
-      const float to = fmaxf(top, mv), w0 = __builtin_amdgcn_exp2f(top - to), w1 = __builtin_amdgcn_exp2f(mv - to);
-      top = to;
-      den = den * w0 + lv * w1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * w0 + load_dev(&a.part_o[at * D + ch + j]) * w1;
-    }
-    store(row, x, den == 0.f ? 0.f : 1.f / den);
+  for (int v = 0; v < kWaves; ++v) top = fmaxf(top, s_red[v]);
+  float den = 0.f;
+  for (int v = tid; v < x.splits; v += 256) {
+    const float2 ml = a.part_ml[base + (int64_t)v * a.rows_per_group];
+    const float w = __builtin_amdgcn_exp2f(ml.x - top);
+    s_w[v] = w;
+    den += w * ml.y;
   }
+  for (int d = 1; d < 64; d <<= 1) den += __shfl_xor(den, d);
+  if (tid % 64 == 0) s_red[kWaves + tid / 64] = den;
+  __syncthreads();
+  den = 0.f;
+#pragma unroll
+  for (int v = 0; v < kWaves; ++v) den += s_red[kWaves + v];
+  f4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int v = strand; v < x.splits; v += STRANDS) {
+    const f4 part = *reinterpret_cast<const f4*>(a.part_o + (base + (int64_t)v * a.rows_per_group) * D + 4 * ch);
+    sum += part * s_w[v];
+  }
+  s_x[strand][ch] = sum;
+  __syncthreads();
+  if (strand > 0) return;
+#pragma unroll
+  for (int v = 1; v < STRANDS; ++v) sum += s_x[v][ch];
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) w[j] = pack16(a.bf16, sum[2 * j] * inv, sum[2 * j + 1] * inv);
+  uint16_t* op = a.o + ((int64_t)(x.first + at / G) * (a.c.heads * G) + hk * G + at % G) * D + 4 * ch;
+  *reinterpret_cast<u2*>(op) = u2{w[0], w[1]};
 }
 
 // How a launch is cut: rows to a workgroup, row groups, chunks of keys.
@@ -530,7 +569,7 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   p.row_groups = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
   p.cells = sequences * heads * p.row_groups;
   const int64_t keys = max_ctx + max_q, unit = kBlock * kWaves;
-  int64_t splits = p.cells > kMaxCells ? 1 : (1024 + p.cells - 1) / p.cells;
+  int64_t splits = (1024 + p.cells - 1) / p.cells;
   const int64_t most = (keys + unit - 1) / unit;
   if (splits > most) splits = most;
   p.chunk = (int)((((keys + splits - 1) / splits) + unit - 1) / unit * unit);
@@ -538,7 +577,7 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   const size_t parts = p.splits > 1 ? (size_t)p.cells * p.splits * 16 * p.rt : 0;
   p.ml_bytes = parts * sizeof(float2);
   p.o_bytes = parts * dim * sizeof(float);
-  p.need = kMaxCells * sizeof(uint32_t) + p.ml_bytes + p.o_bytes;
+  p.need = p.ml_bytes + p.o_bytes;
   return p;
 }
 
@@ -549,6 +588,8 @@ void launch(const AttnPlan& p, const AttnArgs& a, int sequences, hipStream_t s) 
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 2>), grid, dim3(256), 0, s, a);
+  if (p.splits > 1)
+    hipLaunchKernelGGL((tree_attention_join_kernel<D>), dim3((unsigned)p.cells, 16 * p.rt), dim3(256), 0, s, a, p.splits);
 }
 
 }  // namespace
@@ -586,17 +627,17 @@ extern "C" cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_t
   if (mask && mask_words < (max_q + 63) / 64)
     return fail(CL_EINVAL, "attention: %d mask words for %d new tokens", mask_words, max_q);
   const AttnPlan p = plan_attention(sequences, q_heads, cache->heads, cache->dim, max_q, max_ctx);
+  if (p.cells > 0x7FFFFFFF) return fail(CL_ESIZE, "attention: too many sequences and heads");
   if ((int64_t)cache->heads * p.row_groups > 65535) return fail(CL_ESIZE, "attention: too many heads and row groups");
-  if (!work || work_bytes < p.need)
+  if (p.need && (!work || work_bytes < p.need))
     return fail(CL_ENOMEM, "attention: work has %zu bytes, %zu are needed", work_bytes, p.need);
   if (!aligned_to(work, 16)) return fail(CL_EINVAL, "attention: work must be 16-byte aligned");
   uint8_t* w = static_cast<uint8_t*>(work);
   AttnArgs a = {static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), *cache, block_table, ctx_lens, cu_q,
-                reinterpret_cast<const uint64_t*>(mask), reinterpret_cast<uint32_t*>(w),
-                reinterpret_cast<float2*>(w + kMaxCells * sizeof(uint32_t)),
-                reinterpret_cast<float*>(w + kMaxCells * sizeof(uint32_t) + p.ml_bytes),
+                reinterpret_cast<const uint64_t*>(mask), reinterpret_cast<float2*>(w),
+                reinterpret_cast<float*>(w + p.ml_bytes),
                 q_token, q_head, tokens, q_heads / cache->heads, table_width, max_q, mask_words, dtype == CL_BF16,
-                p.chunk, p.row_groups, __builtin_ctz(cache->page_size), scale};
+                p.chunk, p.row_groups, 16 * p.rt, __builtin_ctz(cache->page_size), scale};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (cache->kind == CL_KV_INT8) {
     if (cache->dim == 128)

@@ -217,13 +217,13 @@ class KVCache:
         return k, v
 
     def _workspace(self, sizes):
-        """The workspace for these sizes, zeroed when it is made (the calls leave it zeroed).  One that was
-        outgrown is kept: work on another stream or a recorded graph may still use it."""
+        """The workspace for these sizes.  One that was outgrown is kept: work on another stream or a
+        recorded graph may still use it."""
         need = _lib.cl_tree_attention_work_bytes(*sizes)
         if need and (self._work is None or self._work.numel() < need):
             if self._work is not None:
                 self._outgrown.append(self._work)
-            self._work = _torch.zeros(2 * need, dtype=_torch.uint8, device=self.device)
+            self._work = _torch.empty(2 * need, dtype=_torch.uint8, device=self.device)
         return self._work
 
 

@@ -135,9 +135,8 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  *                    NULL: token t sees new tokens 0..t.  mask_words >= ceil(max_q / 64); bits from n_b on
  *                    are ignored.
  *   scale            of the scores, finite
- *   work             device, cl_tree_attention_work_bytes(...) bytes for these arguments, 16-byte aligned.
- *                    Zeroed once before its first use; every call leaves its counters zero.  One call at a
- *                    time may use it.
+ *   work             device, cl_tree_attention_work_bytes(...) bytes for these arguments, 16-byte aligned (may be
+ *                    NULL where that is 0).  Holds anything before and after; one call at a time may use it.
  * Scores, maxima, sums and outputs are held in fp32.  The probabilities enter the matrix cores as fp16,
  * scaled so that no value down to 2^-29 of the largest is lost; keys and values enter exactly.
  * A page of block_table outside the cache, or a place past its width, gives NaN in the rows that see it.
