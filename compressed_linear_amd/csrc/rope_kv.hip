@@ -1,5 +1,7 @@
 // rope_kv.hip -- rotary positions and the quantised K/V cache: its table,
 // the rotation, appending tokens and reading them back.
+#include <type_traits>
+
 #include "serving.h"
 
 namespace cl {
@@ -46,9 +48,9 @@ struct RopeArgs {
   int tokens, heads, dim, rot, layout, table_rows;
 };
 
-// One thread a pair of channels, rotated or copied.
+// Any alignment: one thread a pair of channels, rotated or copied.
 template <int IN, int OUT>
-__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
   const int pairs = (a.dim + 1) / 2, half = a.rot / 2;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= (int64_t)a.tokens * a.heads * pairs) return;
@@ -73,6 +75,63 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   if (c2 != c1) y[c2] = Elem<OUT>::down(v);
 }
 
+// 16-byte pieces: a thread owns 16 channels of a head -- eight pairs, as two runs of 8 channels in either layout, or
+// 16 channels that are copied -- and does them for HEADS heads of its token, so that the cosines and sines
+// (64 bytes, against 32 to 64 of a head) are read once.  Bound by memory.
+template <int IN, int OUT, int HEADS>
+__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
+  const int units = a.dim / 16, half = a.rot / 2, blocks = (a.heads + HEADS - 1) / HEADS;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= (int64_t)a.tokens * blocks * units) return;
+  const int u = (int)(at % units), hb = (int)(at / units % blocks), t = (int)(at / units / blocks);
+  const bool turned = 16 * u < a.rot;
+  int c1 = 16 * u, c2 = c1 + 8;
+  float2 cs[8];
+  if (turned) {
+    if (a.layout == CL_ROPE_HALF) c1 = 8 * u, c2 = c1 + half;
+    const int p = a.positions[t];
+    if (p >= 0 && p < a.table_rows) {
+      const float4* row = reinterpret_cast<const float4*>(a.table + (int64_t)p * half + 8 * u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = row[i];
+        cs[2 * i] = make_float2(v.x, v.y), cs[2 * i + 1] = make_float2(v.z, v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs[i] = make_float2(kNan, kNan);
+    }
+  }
+  const auto* x = static_cast<const typename Elem<IN>::raw*>(a.x) + t * a.x_token;
+  auto* y = static_cast<typename Elem<OUT>::raw*>(a.y) + t * a.y_token;
+  const int h0 = hb * HEADS;
+  float v1[HEADS][8], v2[HEADS][8];
+#pragma unroll
+  for (int k = 0; k < HEADS; ++k) {
+    if (h0 + k >= a.heads) break;
+    load8<IN>(x + (h0 + k) * a.x_head + c1, v1[k]);
+    load8<IN>(x + (h0 + k) * a.x_head + c2, v2[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < HEADS; ++k) {
+    if (h0 + k >= a.heads) break;
+    if (turned) {
+      if (a.layout == CL_ROPE_HALF) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rotate_pair(v1[k][i], v2[k][i], cs[i].x, cs[i].y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          rotate_pair(v1[k][2 * i], v1[k][2 * i + 1], cs[i].x, cs[i].y);
+          rotate_pair(v2[k][2 * i], v2[k][2 * i + 1], cs[4 + i].x, cs[4 + i].y);
+        }
+      }
+    }
+    store8<OUT>(y + (h0 + k) * a.y_head + c1, v1[k]);
+    store8<OUT>(y + (h0 + k) * a.y_head + c2, v2[k]);
+  }
+}
+
 // ------------------------------------------------------------------ append
 struct AppendArgs {
   cl_kv_cache c;
@@ -81,125 +140,242 @@ struct AppendArgs {
   const int32_t* slots;
   const int32_t* positions;
   const float2* table;  // NULL: no rotation
-  int tokens, rot, layout, table_rows;
+  int tokens, rot, layout, table_rows, page_shift;
 };
 
-__device__ __forceinline__ int64_t cache_row(const cl_kv_cache& c, int slot, int head) {
-  const int page = slot / c.page_size;
-  return ((int64_t)page * c.heads + head) * c.page_size + slot % c.page_size;
+// Eight channels from `at` of a head at x; VEC: as two 16-byte (fp32) or one load, otherwise one by one.
+template <int IN, bool VEC>
+__device__ __forceinline__ void channels8(const typename Elem<IN>::raw* x, int at, float (&v)[8]) {
+  if constexpr (VEC) {
+    load8<IN>(x + at, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<IN>::up(x[at + i]);
+  }
 }
 
-// One wavefront a (token, head, k or v); lane l holds channels 2l and 2l + 1.
-template <int IN, int KIND>
-__global__ void __launch_bounds__(64) kv_append_kernel(AppendArgs a) {
-  const int t = blockIdx.x, h = blockIdx.y, which = blockIdx.z, l = threadIdx.x;
+// Largest value over the 16 lanes of a row (all get it), or over 8 or 4 of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+  const auto step = [](float x, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  v = fmaxf(v, step(v, std::integral_constant<int, 0xB1>()));                            // quad_perm [1, 0, 3, 2]
+  v = fmaxf(v, step(v, std::integral_constant<int, 0x4E>()));                            // quad_perm [2, 3, 0, 1]
+  if constexpr (LANES >= 8) v = fmaxf(v, step(v, std::integral_constant<int, 0x141>()));   // mirrored in 8
+  if constexpr (LANES >= 16) v = fmaxf(v, step(v, std::integral_constant<int, 0x140>()));  // mirrored in 16
+  return v;
+}
+
+// D / 8 lanes a (token, head, k or v), eight channels each; a workgroup has the rows of consecutive tokens of one
+// head, whose scales and, in a page, codes lie together.  Bound by memory for prompts, by the launch for steps.
+template <int IN, int KIND, int D, bool VEC>
+__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
+  constexpr int LANES = D / 8;
+  const int h = blockIdx.y, which = blockIdx.z, t = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int ch = 8 * (threadIdx.x % LANES);
+  if (t >= a.tokens) return;
   const int slot = a.slots[t];
-  if (slot < 0 || slot >= a.c.pages * a.c.page_size) return;
-  const int D = a.c.dim, half = a.rot / 2;
+  if (slot < 0 || slot >= a.c.pages << a.page_shift) return;
   const auto* x = static_cast<const typename Elem<IN>::raw*>(a.src[which]) + t * a.token[which] + h * a.head[which];
-  float v[2] = {0.f, 0.f};
-  const bool rotated = a.table && which == 0;
-  const int p = rotated ? a.positions[t] : 0;
-  const bool in = !rotated || (p >= 0 && p < a.table_rows);
-  for (int j = 0; j < 2; ++j) {
-    const int ch = 2 * l + j;
-    if (ch >= D || !in) continue;
-    float own = Elem<IN>::up(x[ch]);
-    if (rotated && ch < a.rot) {
-      const int i = a.layout == CL_ROPE_HALF ? ch % half : ch / 2;
-      int c1, c2;
-      pair_of(a.layout, half, i, &c1, &c2);
-      float u = Elem<IN>::up(x[c1]), w = Elem<IN>::up(x[c2]);
-      const float2 cs = a.table[(int64_t)p * half + i];
-      rotate_pair(u, w, cs.x, cs.y);
-      own = ch == c1 ? u : w;
+  float v[8];
+  channels8<IN, VEC>(x, ch, v);
+  if (a.table && which == 0) {
+    const int p = a.positions[t], half = a.rot / 2;
+    const bool in = p >= 0 && p < a.table_rows;
+    const float2* cs = a.table + (int64_t)(in ? p : 0) * half;
+    if (!in) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    } else if (VEC && a.layout == CL_ROPE_HALF) {  // half is a multiple of 8: the partners are 8 channels too
+      if (ch < a.rot) {
+        const bool low = ch < half;
+        float w[8];
+        channels8<IN, VEC>(x, low ? ch + half : ch - half, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 c = cs[(low ? ch : ch - half) + i];
+          float p1 = low ? v[i] : w[i], p2 = low ? w[i] : v[i];
+          rotate_pair(p1, p2, c.x, c.y);
+          v[i] = low ? p1 : p2;
+        }
+      }
+    } else if (VEC) {
+      if (ch < a.rot) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 c = cs[ch / 2 + i];
+          rotate_pair(v[2 * i], v[2 * i + 1], c.x, c.y);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (ch + i >= a.rot) continue;
+        const int pr = a.layout == CL_ROPE_HALF ? (ch + i) % half : (ch + i) / 2;
+        int c1, c2;
+        pair_of(a.layout, half, pr, &c1, &c2);
+        float p1 = Elem<IN>::up(x[c1]), p2 = Elem<IN>::up(x[c2]);
+        rotate_pair(p1, p2, cs[pr].x, cs[pr].y);
+        v[i] = ch + i == c1 ? p1 : p2;
+      }
     }
-    v[j] = own == own ? own : 0.f;
   }
-  float m = fmaxf(fabsf(v[0]), fabsf(v[1]));
-  const int width = KIND == CL_KV_INT8 ? 64 : 16;  // lanes of a scale: a head, or 32 channels
-  for (int d = 1; d < width; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const int64_t row = cache_row(a.c, slot, h);
-  uint8_t* out = static_cast<uint8_t*>(which ? a.c.v : a.c.k);
-  uint16_t* sc = which ? a.c.v_scale : a.c.k_scale;
-  const int most = KIND == CL_KV_INT8 ? 127 : 7;
-  float s = fminf(m / (float)most, KIND == CL_KV_INT8 ? 65504.f : 8192.f);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = v[i] == v[i] ? v[i] : 0.f;  // a NaN counts as 0
+    m = fmaxf(m, fabsf(v[i]));
+  }
+  m = lanes_max<KIND == CL_KV_INT8 ? LANES : 4>(m);  // a scale's lanes: a head, or 32 channels
+  constexpr float most = KIND == CL_KV_INT8 ? 127.f : 7.f;
+  float s = fminf(m / most, KIND == CL_KV_INT8 ? 65504.f : 8192.f);
   if (KIND == CL_KV_INT4) s = (float)(__bf16)s;
   const _Float16 s16 = (_Float16)s;
   const float r = (float)s16 > 0.f ? 1.0f / (float)s16 : 0.f;
-  int q[2];
-  for (int j = 0; j < 2; ++j) {
-    const float c = r > 0.f ? rintf(v[j] * r) : 0.f;
-    q[j] = (int)fminf(fmaxf(c, (float)-most), (float)most);
+  uint32_t q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // an infinity times 0 would be NaN, but then the scale is not 0
+    const float c = fminf(fmaxf(rintf(v[i] * r), -most), most);
+    q[i] = (uint32_t)(int)(c + (KIND == CL_KV_INT8 ? 128.f : 8.f));
   }
-  if (2 * l >= D) return;
+  const int64_t row = (((int64_t)(slot >> a.page_shift) * a.c.heads + h) << a.page_shift) + (slot & (a.c.page_size - 1));
+  uint8_t* out = static_cast<uint8_t*>(which ? a.c.v : a.c.k);
+  uint16_t* sc = which ? a.c.v_scale : a.c.k_scale;
   if (KIND == CL_KV_INT8) {
-    out[row * D + 2 * l] = (uint8_t)(q[0] + 128);
-    out[row * D + 2 * l + 1] = (uint8_t)(q[1] + 128);
-    if (l == 0) sc[row] = __builtin_bit_cast(uint16_t, s16);
+    *reinterpret_cast<w2*>(out + row * D + ch) =
+        w2{q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24};
+    if (ch == 0) sc[row] = __builtin_bit_cast(uint16_t, s16);
   } else {
-    out[row * (D / 2) + l] = (uint8_t)((q[0] + 8) | (q[1] + 8) << 4);
-    if (l % 16 == 0) sc[row * (D / 32) + l / 16] = __builtin_bit_cast(uint16_t, s16);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= q[i] << (4 * i);
+    *reinterpret_cast<uint32_t*>(out + row * (D / 2) + ch / 2) = w;
+    if (ch % 32 == 0) sc[row * (D / 32) + ch / 32] = __builtin_bit_cast(uint16_t, s16);
   }
 }
 
 // -------------------------------------------------------------------- read
-// One thread a channel of K and of V.
-template <int OUT, int KIND>
-__global__ void __launch_bounds__(256) kv_read_kernel(cl_kv_cache c, const int32_t* __restrict__ slots, int n,
+// D / 8 lanes a (slot, head), eight channels of K and of V each; a workgroup has the rows of consecutive slots of
+// one head, two to a thread.  Bound by memory.
+template <int OUT, int KIND, int D>
+__global__ void __launch_bounds__(256) kv_read_kernel(cl_kv_cache c, int page_shift, const int32_t* __restrict__ slots, int n,
                                                       typename Elem<OUT>::raw* __restrict__ ko,
                                                       typename Elem<OUT>::raw* __restrict__ vo) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int D = c.dim;
-  if (at >= (int64_t)n * c.heads * D) return;
-  const int ch = (int)(at % D), h = (int)(at / D % c.heads), t = (int)(at / D / c.heads);
-  const int slot = slots[t];
-  float v[2] = {0.f, 0.f};
-  if (slot >= 0 && slot < c.pages * c.page_size) {
-    const int64_t row = cache_row(c, slot, h);
+  constexpr int LANES = D / 8, ROWS = 256 / LANES, PER = 2;
+  const int h = blockIdx.y, ch = 8 * (threadIdx.x % LANES);
+  const int t0 = blockIdx.x * (ROWS * PER) + threadIdx.x / LANES;
+  w2 code[PER][2];
+  float scale[PER][2];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int t = t0 + k * ROWS;
+    const int slot = t < n ? slots[t] : -1;
+    const bool in = slot >= 0 && slot < c.pages << page_shift;
+    const int64_t row = in ? (((int64_t)(slot >> page_shift) * c.heads + h) << page_shift) + (slot & (c.page_size - 1)) : 0;
+#pragma unroll
     for (int w = 0; w < 2; ++w) {
       const uint8_t* b = static_cast<const uint8_t*>(w ? c.v : c.k);
       const uint16_t* s = w ? c.v_scale : c.k_scale;
-      if (KIND == CL_KV_INT8) {
-        v[w] = (float)((int)b[row * D + ch] - 128) * Elem<CL_F16>::up(s[row]);
+      if constexpr (KIND == CL_KV_INT8) {
+        code[k][w] = *reinterpret_cast<const w2*>(b + row * D + ch);
+        scale[k][w] = Elem<CL_F16>::up(s[row]);
       } else {
-        const int nib = (b[row * (D / 2) + ch / 2] >> (ch % 2 * 4)) & 15;
-        v[w] = (float)(nib - 8) * Elem<CL_F16>::up(s[row * (D / 32) + ch / 32]);
+        code[k][w].x = *reinterpret_cast<const uint32_t*>(b + row * (D / 2) + ch / 2);
+        scale[k][w] = Elem<CL_F16>::up(s[row * (D / 32) + ch / 32]);
       }
+      if (!in) scale[k][w] = 0.f;
     }
   }
-  ko[at] = Elem<OUT>::down(v[0]);
-  vo[at] = Elem<OUT>::down(v[1]);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int t = t0 + k * ROWS;
+    if (t >= n) break;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = KIND == CL_KV_INT8 ? (int)((code[k][w][i / 4] >> (8 * (i % 4))) & 255) - 128
+                                         : (int)((code[k][w].x >> (4 * i)) & 15) - 8;
+        v[i] = (float)q * scale[k][w];
+      }
+      store8<OUT>((w ? vo : ko) + ((int64_t)t * c.heads + h) * D + ch, v);
+    }
+  }
+}
+
+template <int IN, int OUT>
+void launch_rope(const RopeArgs& a, hipStream_t s) {
+  const bool vec = a.rot % 16 == 0 && a.dim % 16 == 0 && aligned_to(a.table, 16) &&
+                   heads_aligned(a.x, IN, a.x_token, a.x_head) && heads_aligned(a.y, OUT, a.y_token, a.y_head);
+  const auto grid = [](int64_t n) { return dim3((unsigned)((n + 255) / 256)); };
+  if (!vec)
+    hipLaunchKernelGGL((rope_pair_kernel<IN, OUT>), grid((int64_t)a.tokens * a.heads * ((a.dim + 1) / 2)), dim3(256), 0, s, a);
+  else if ((int64_t)a.tokens * a.heads >= 32768)  // enough threads to fill the card with four heads each
+    hipLaunchKernelGGL((rope_kernel<IN, OUT, 4>), grid((int64_t)a.tokens * ((a.heads + 3) / 4) * (a.dim / 16)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((rope_kernel<IN, OUT, 1>), grid((int64_t)a.tokens * a.heads * (a.dim / 16)), dim3(256), 0, s, a);
 }
 
 template <int IN>
-void launch_rope(int out, const RopeArgs& a, unsigned grid, hipStream_t s) {
+void launch_rope(int out, const RopeArgs& a, hipStream_t s) {
   if (out == CL_F16)
-    hipLaunchKernelGGL((rope_kernel<IN, CL_F16>), dim3(grid), dim3(256), 0, s, a);
+    launch_rope<IN, CL_F16>(a, s);
   else if (out == CL_BF16)
-    hipLaunchKernelGGL((rope_kernel<IN, CL_BF16>), dim3(grid), dim3(256), 0, s, a);
+    launch_rope<IN, CL_BF16>(a, s);
   else
-    hipLaunchKernelGGL((rope_kernel<IN, CL_F32>), dim3(grid), dim3(256), 0, s, a);
+    launch_rope<IN, CL_F32>(a, s);
+}
+
+template <int IN, int KIND, int D>
+void launch_append(const AppendArgs& a, hipStream_t s) {
+  const bool vec = heads_aligned(a.src[0], IN, a.token[0], a.head[0]) && heads_aligned(a.src[1], IN, a.token[1], a.head[1]) &&
+                   a.rot % 16 == 0;
+  const dim3 grid((unsigned)(((int64_t)a.tokens * (D / 8) + 255) / 256), a.c.heads, 2);
+  if (vec)
+    hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, false>), grid, dim3(256), 0, s, a);
 }
 
 template <int IN>
 void launch_append(const AppendArgs& a, hipStream_t s) {
-  const dim3 grid(a.tokens, a.c.heads, 2);
-  if (a.c.kind == CL_KV_INT8)
-    hipLaunchKernelGGL((kv_append_kernel<IN, CL_KV_INT8>), grid, dim3(64), 0, s, a);
-  else
-    hipLaunchKernelGGL((kv_append_kernel<IN, CL_KV_INT4>), grid, dim3(64), 0, s, a);
+  if (a.c.kind == CL_KV_INT8) {
+    if (a.c.dim == 128)
+      launch_append<IN, CL_KV_INT8, 128>(a, s);
+    else
+      launch_append<IN, CL_KV_INT8, 64>(a, s);
+  } else {
+    if (a.c.dim == 128)
+      launch_append<IN, CL_KV_INT4, 128>(a, s);
+    else
+      launch_append<IN, CL_KV_INT4, 64>(a, s);
+  }
+}
+
+template <int OUT, int KIND, int D>
+void launch_read(const cl_kv_cache& c, const int32_t* slots, int n, void* ko, void* vo, hipStream_t s) {
+  typedef typename Elem<OUT>::raw raw;
+  const int rows = 2 * 256 / (D / 8);
+  hipLaunchKernelGGL((kv_read_kernel<OUT, KIND, D>), dim3((unsigned)(((int64_t)n + rows - 1) / rows), c.heads), dim3(256), 0, s,
+                     c, __builtin_ctz(c.page_size), slots, n, static_cast<raw*>(ko), static_cast<raw*>(vo));
 }
 
 template <int OUT>
-void launch_read(const cl_kv_cache& c, const int32_t* slots, int n, void* ko, void* vo, unsigned grid, hipStream_t s) {
-  typedef typename Elem<OUT>::raw raw;
-  if (c.kind == CL_KV_INT8)
-    hipLaunchKernelGGL((kv_read_kernel<OUT, CL_KV_INT8>), dim3(grid), dim3(256), 0, s, c, slots, n,
-                       static_cast<raw*>(ko), static_cast<raw*>(vo));
-  else
-    hipLaunchKernelGGL((kv_read_kernel<OUT, CL_KV_INT4>), dim3(grid), dim3(256), 0, s, c, slots, n,
-                       static_cast<raw*>(ko), static_cast<raw*>(vo));
+void launch_read(const cl_kv_cache& c, const int32_t* slots, int n, void* ko, void* vo, hipStream_t s) {
+  if (c.kind == CL_KV_INT8) {
+    if (c.dim == 128)
+      launch_read<OUT, CL_KV_INT8, 128>(c, slots, n, ko, vo, s);
+    else
+      launch_read<OUT, CL_KV_INT8, 64>(c, slots, n, ko, vo, s);
+  } else {
+    if (c.dim == 128)
+      launch_read<OUT, CL_KV_INT4, 128>(c, slots, n, ko, vo, s);
+    else
+      launch_read<OUT, CL_KV_INT4, 64>(c, slots, n, ko, vo, s);
+  }
 }
 
 // Workgroups of 256 threads for n threads; 0 where the grid would be too large.
@@ -269,15 +445,14 @@ extern "C" cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, in
   if ((int64_t)tokens * heads >= ((int64_t)1 << 40) / dim) return fail(CL_ESIZE, "rope: tokens * heads * dim at 2^40 or more");
   const RopeArgs a = {x, y, positions, reinterpret_cast<const float2*>(table), x_token, x_head, y_token, y_head,
                       tokens, heads, dim, rot, layout, table_rows};
-  const unsigned grid = grid_of((int64_t)tokens * heads * ((dim + 1) / 2));
-  if (!grid) return fail(CL_ESIZE, "rope: too many tokens");
+  if (!grid_of((int64_t)tokens * heads * ((dim + 1) / 2))) return fail(CL_ESIZE, "rope: too many tokens");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (x_dtype == CL_F16)
-    launch_rope<CL_F16>(y_dtype, a, grid, s);
+    launch_rope<CL_F16>(y_dtype, a, s);
   else if (x_dtype == CL_BF16)
-    launch_rope<CL_BF16>(y_dtype, a, grid, s);
+    launch_rope<CL_BF16>(y_dtype, a, s);
   else
-    launch_rope<CL_F32>(y_dtype, a, grid, s);
+    launch_rope<CL_F32>(y_dtype, a, s);
   return launched("rope");
 }
 
@@ -296,7 +471,7 @@ extern "C" cl_status cl_kv_append(const cl_kv_cache* cache, const void* k, const
     return fail(CL_EINVAL, "append: a pointer is misaligned for its type");
   if (table && (st = check_rope(positions, table, table_rows, rot, layout, cache->dim)) != CL_OK) return st;
   const AppendArgs a = {*cache, {k, v}, {k_token, v_token}, {k_head, v_head}, slots, positions,
-                        reinterpret_cast<const float2*>(table), tokens, table ? rot : 0, layout, table_rows};
+                        reinterpret_cast<const float2*>(table), tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size)};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)
     launch_append<CL_F16>(a, s);
@@ -318,14 +493,12 @@ extern "C" cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, 
   if (!slots || !k_out || !v_out) return fail(CL_EINVAL, "read: a required pointer is NULL");
   if (!aligned_to(k_out, 16) || !aligned_to(v_out, 16) || !aligned_to(slots, 4))
     return fail(CL_EINVAL, "read: outputs must be 16-byte aligned");
-  const unsigned grid = grid_of((int64_t)n * cache->heads * cache->dim);
-  if (!grid) return fail(CL_ESIZE, "read: too many slots");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)
-    launch_read<CL_F16>(*cache, slots, n, k_out, v_out, grid, s);
+    launch_read<CL_F16>(*cache, slots, n, k_out, v_out, s);
   else if (dtype == CL_BF16)
-    launch_read<CL_BF16>(*cache, slots, n, k_out, v_out, grid, s);
+    launch_read<CL_BF16>(*cache, slots, n, k_out, v_out, s);
   else
-    launch_read<CL_F32>(*cache, slots, n, k_out, v_out, grid, s);
+    launch_read<CL_F32>(*cache, slots, n, k_out, v_out, s);
   return launched("read");
 }

@@ -31,6 +31,46 @@ struct Elem<CL_F32> {
   static __device__ __forceinline__ raw down(float f) { return f; }
 };
 
+typedef float v4 __attribute__((ext_vector_type(4)));
+typedef uint32_t w4 __attribute__((ext_vector_type(4)));
+typedef uint32_t w2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half_pair __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
+
+// Two values rounded to 16 bits, in one word.
+template <int DT>
+__device__ __forceinline__ uint32_t down2(float x, float y) {
+  if constexpr (DT == CL_F16)
+    return __builtin_bit_cast(uint32_t, half_pair{(_Float16)x, (_Float16)y});
+  else
+    return __builtin_bit_cast(uint32_t, bf16_pair{(__bf16)x, (__bf16)y});
+}
+
+// Eight contiguous elements, 16-byte aligned.
+template <int DT>
+__device__ __forceinline__ void load8(const typename Elem<DT>::raw* p, float (&v)[8]) {
+  if constexpr (DT == CL_F32) {
+    const v4* q = reinterpret_cast<const v4*>(p);
+    const v4 a = q[0], b = q[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  } else {
+    const w4 a = *reinterpret_cast<const w4*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<DT>::up((uint16_t)(a[i / 2] >> (16 * (i % 2))));
+  }
+}
+template <int DT>
+__device__ __forceinline__ void store8(typename Elem<DT>::raw* p, const float (&v)[8]) {
+  if constexpr (DT == CL_F32) {
+    v4* q = reinterpret_cast<v4*>(p);
+    q[0] = v4{v[0], v[1], v[2], v[3]};
+    q[1] = v4{v[4], v[5], v[6], v[7]};
+  } else {
+    *reinterpret_cast<w4*>(p) = w4{down2<DT>(v[0], v[1]), down2<DT>(v[2], v[3]), down2<DT>(v[4], v[5]), down2<DT>(v[6], v[7])};
+  }
+}
+
 inline size_t elem_size(int dtype) { return dtype == CL_F32 ? 4 : 2; }
 inline bool elem_ok(int dtype) { return dtype == CL_F16 || dtype == CL_BF16 || dtype == CL_F32; }
 inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -59,6 +99,12 @@ inline cl_status check_rope(const int32_t* positions, const float* table, int ta
   if (rot < 2 || rot % 2 || rot > dim) return fail(CL_EINVAL, "rope: rot %d is odd or not in [2, %d]", rot, dim);
   if (layout != CL_ROPE_HALF && layout != CL_ROPE_INTERLEAVED) return fail(CL_EINVAL, "rope: unknown layout %d", layout);
   return CL_OK;
+}
+
+// Whether every head of a tensor starts on a 16-byte boundary.
+inline bool heads_aligned(const void* p, int dtype, int64_t token, int64_t head) {
+  const int64_t e = (int64_t)elem_size(dtype);
+  return aligned_to(p, 16) && token * e % 16 == 0 && head * e % 16 == 0;
 }
 
 inline cl_status launched(const char* what) {
