@@ -8,9 +8,12 @@
 // takes the keys 32 at a time.  In S^T a lane owns one row and 4 + 4 keys; those
 // eight probabilities are, in the same lane and order, its part of the second
 // product's operand, so P never leaves the registers.  The contraction may run
-// over channels and keys in any order that both operands follow: K is read in 16-byte
-// pieces of a key's channels, V in pieces of 8 channels of each of a lane's
-// eight keys, which v_perm transposes while it widens the codes.
+// over channels and keys in any order that both operands follow: a lane takes K in 16-byte
+// pieces of a key's channels, V in pieces of 8 channels of each of its
+// eight keys, which v_perm transposes while it widens the codes.  The lanes of an operand are
+// neighbours in key, not in memory, so the blocks come through LDS: asked for a
+// step ahead straight into it, moved to registers when they are there (loads of the
+// operand's own layout cost an access for every lane: 64 sequences of up to 8192 tokens took 147 us with them).
 //
 // Exactness: int8 codes are fp16 values (the byte as a subnormal, one packed fma
 // makes it code * 2^-9), their scales go to the fp32 scores (K) and to the
@@ -43,6 +46,7 @@ constexpr float kNone = -3.4e38f;  // running maximum before any key
 constexpr float kSlack = 4.f;      // log2 by which a score may pass the running maximum
 constexpr int kProbBits = 11;      // probabilities are scaled by 2^11: with the slack at most 2^15
 
+constexpr int kMaxChunk = 2048;    // keys of a workgroup
 constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
 
 struct AttnArgs {
@@ -76,18 +80,21 @@ __device__ __forceinline__ uint32_t pack16(int bf16, float x, float y) {
 // `max_splits` (a sequence longer than the launch was sized for gets longer chunks).
 struct Range {
   int first, n_new, ctx, splits;
-  int64_t n, chunk;
+  uint32_t n, chunk;
 };
-__device__ __forceinline__ Range range_of(const AttnArgs& a, int b, int max_splits) {
+__device__ __forceinline__ Range range_of(const AttnArgs& a, int first, int end, int ctx, int max_splits) {
   Range x;
-  x.first = a.cu_q[b];
-  const int64_t n_new = (int64_t)a.cu_q[b + 1] - x.first;
+  x.first = first;
+  const int64_t n_new = (int64_t)end - x.first;
   x.n_new = x.first < 0 || n_new < 0 || n_new > a.max_q || x.first + n_new > a.tokens ? 0 : (int)n_new;
-  x.ctx = max(a.ctx_lens[b], 0);
-  x.n = (int64_t)x.ctx + x.n_new;
-  const int64_t least = (x.n + max_splits - 1) / max_splits;
-  x.chunk = least <= a.chunk ? a.chunk : (least + kBlock * kWaves - 1) / (kBlock * kWaves) * (kBlock * kWaves);
-  x.splits = (int)((x.n + x.chunk - 1) / x.chunk);
+  x.ctx = max(ctx, 0);
+  x.n = (uint32_t)x.ctx + x.n_new;
+  x.chunk = a.chunk;
+  if (x.n > x.chunk * (uint64_t)max_splits) {
+    const uint32_t least = (x.n - 1) / max_splits + 1;
+    x.chunk = (least + kBlock * kWaves - 1) / (kBlock * kWaves) * (kBlock * kWaves);
+  }
+  x.splits = x.n ? (int)((x.n - 1) / x.chunk + 1) : 0;
   return x;
 }
 
@@ -115,22 +122,17 @@ __device__ __forceinline__ uint32_t widen4(uint32_t word, int at, h2 s) {
   return __builtin_bit_cast(uint32_t, c * s);
 }
 
-// What a wavefront loads for one block of 32 keys.
-template <int KIND, int D>
-struct Block;
-
-template <int D>
-struct Block<CL_KV_INT8, D> {
-  u4 k[2][D / 64];  // tile, piece: key l % 16, channels 64 piece + 16 (l / 16) ..
-  u2 v[8];          // key 4 (l / 16) + i of either tile, channels (D / 16) (l % 16) ..  (D = 64: 4 channels, x only)
-  u2 ks[2], vs[2];  // fp16 scales of keys 4 (l / 16) .. of either tile
+// The scales of a block of 32 keys, two tiles of 16, that a lane needs.
+template <int KIND>
+struct Scales;
+template <>
+struct Scales<CL_KV_INT8> {
+  u2 k[2], v[2];  // fp16, of keys 4 (l / 16) .. of either tile
 };
-
-template <int D>
-struct Block<CL_KV_INT4, D> {
-  u4 k[2];           // key l % 16, channels (D / 4) (l / 16) ..  (D = 64: 16 channels, x and y only)
-  uint32_t v[8];     // key 4 (l / 16) + i, channels (D / 16) (l % 16) ..  (D = 64: 4 channels, the low half)
-  uint16_t ks[2], vs[8];
+template <>
+struct Scales<CL_KV_INT4> {
+  uint16_t k[2];  // of key l % 16, the lane's channels
+  uint16_t v[8];  // of keys 4 (l / 16) .. of either tile, the lane's channels
 };
 
 // Channel of step s, slot j (0..7) of lane group g in the first product.
@@ -139,43 +141,171 @@ __device__ __forceinline__ constexpr int q_channel(int s, int g) {
   return KIND == CL_KV_INT8 ? (s / 2) * 64 + 16 * g + (s % 2) * 8 : (D / 4) * g + 8 * s;
 }
 
+// 16 bytes of each lane straight into LDS, lane l's at `to` + 16 l; not kept in the caches (aux 2), which is worth a tenth of
+// the rate on long contexts: 64 sequences of up to 8192 tokens 142 -> 127 us.
+__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)from, (__attribute__((address_space(3))) void*)to,
+                                   16, 0, 2);
+}
+
+// Waits for every load asked for so far, those into LDS among them.
+__device__ __forceinline__ void wait_loads() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// Waits for the reads of LDS, so that a load may overwrite what they read.
+__device__ __forceinline__ void wait_lds() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 template <int KIND, int D, int RT>
-__global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   constexpr int STEPS = D / 32;  // matrix-core steps of a score tile
   constexpr int CB = D / 16;     // channel blocks of the output; lane c of a block's 16 rows is channel CB c + block
   constexpr int ROWS = 16 * RT, STRIDE = D + 4;
-  __shared__ __align__(16) float s_o[kWaves][ROWS][STRIDE];
+  constexpr int ROWB = KIND == CL_KV_INT8 ? D : D / 2;  // bytes of a (token, head)
+  constexpr int SC = KIND == CL_KV_INT8 ? 1 : D / 32;
+  constexpr int PIECES = ROWB / 16, TILEB = 16 * ROWB;
+  // a block of K and V of each wavefront, and later its output
+  constexpr int BLOCKB = 4 * TILEB;
+  constexpr size_t KVBYTES = (size_t)kWaves * BLOCKB, OBYTES = (size_t)kWaves * ROWS * STRIDE * 4;
+  __shared__ __align__(1024) uint8_t s_mem[KVBYTES > OBYTES ? KVBYTES : OBYTES];
+  float (*const s_o)[ROWS][STRIDE] = reinterpret_cast<float (*)[ROWS][STRIDE]>(s_mem);
   __shared__ float2 s_ml[kWaves][ROWS];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, c16 = l & 15, g = l >> 4;
-  const int b = blockIdx.z, hk = blockIdx.y % a.c.heads, rg = blockIdx.y / a.c.heads;
-  const Range range = range_of(a, b, gridDim.x);
-  const int first = range.first, n_new = range.n_new, ctx = range.ctx, splits = range.splits, split = blockIdx.x;
-  const int64_t n = range.n, chunk = range.chunk;
+  const int b = blockIdx.y, hk = blockIdx.x % a.c.heads, rg = blockIdx.x / a.c.heads;
+  const int split = blockIdx.z;
+
+  // pages of the wavefront's next 64 tiles of 16 keys, one to a lane: -1 outside the cache or the table
+  int pages = 0;
+  const auto load_pages = [&](uint32_t from, int i) {
+    const uint32_t at = from + (uint32_t)(wave + kWaves * (i + (l >> 1))) * kBlock + 16 * (l & 1);
+    const uint32_t col = at >> a.page_shift;
+    int p = col < (uint32_t)a.table_width ? a.block_table[(int64_t)b * a.table_width + col] : -1;
+    pages = p < a.c.pages ? p : -1;
+  };
+  // the first of them are asked for together with the lengths, which they do not wait for
+  load_pages((uint32_t)split * a.chunk, 0);
+  const Range range = range_of(a, a.cu_q[b], a.cu_q[b + 1], a.ctx_lens[b], gridDim.z);
+  const int first = range.first, n_new = range.n_new, ctx = range.ctx, splits = range.splits;
+  const uint32_t n = range.n, chunk = range.chunk;
   const int G = a.group, rows = min(n_new * G - rg * ROWS, ROWS);  // rows of this workgroup that exist
   if (rows <= 0 || split >= splits) return;
-  const int64_t k0 = split * chunk;
-  const int blocks = (int)((min(n, k0 + chunk) - k0 + kBlock - 1) / kBlock);
+  const uint32_t k0 = split * chunk;  // 32-bit places: a sequence has fewer than 2^31 + 256 tokens
+  const int blocks = (int)((min(n - k0, chunk) + kBlock - 1) / kBlock);
+  if (chunk != (uint32_t)a.chunk) load_pages(k0, 0);
 
-  // ---- Q: rows n = l % 16 of each tile, scaled by a power of two, as the second operand
-  uint32_t q[RT][STEPS][4];
-  float rowc[RT];
+  const uint8_t* const kb = static_cast<const uint8_t*>(a.c.k);
+  const uint8_t* const vb = static_cast<const uint8_t*>(a.c.v);
+  const int tiles_shift = a.page_shift - 4;  // tiles in a page
+  // The path through LDS: lane l of a load fills bytes 16 l .. of its kilobyte and picks its global address to suit.
+  // A 16-byte piece j of row r of a K tile lies at place j ^ swizzle(r) of its row, which spreads the 16 rows that 16
+  // lanes read together over all banks; row r of a V tile lies at row turn(r), which does so for the rows
+  // 0, 4, 8, 12 that four lane groups read together (turn is its own inverse).
+  const auto swizzle = [](uint32_t r) -> uint32_t { return (r * ROWB / 256) & (PIECES - 1); };
+  const auto turn = [](uint32_t r) -> uint32_t { return r ^ ((r >> 2) & 3); };
+  uint8_t* const buf = s_mem + wave * BLOCKB;
+  constexpr int LOADS = TILEB >= 1024 ? TILEB / 1024 : 1;  // of a tile; where a tile is half a load (dim 64 int4), of two
+  uint32_t kfrom[LOADS], vfrom[LOADS];
+#pragma unroll
+  for (int q = 0; q < LOADS; ++q) {
+    const uint32_t r = (q * 64 + l) / PIECES % 16, j = l % PIECES;
+    kfrom[q] = r * ROWB + ((j ^ swizzle(r)) << 4);
+    vfrom[q] = turn(r) * ROWB + (j << 4);
+  }
+  // where the lane reads: of K, key l % 16, its first piece (its second one, for 128-byte rows, is 4 pieces on); of V, key
+  // 4 (l / 16) + j, a sixteenth of the row
+  const uint32_t kread = c16 * ROWB + (((KIND == CL_KV_INT4 && D == 64 ? g / 2 : g) ^ swizzle(c16)) << 4) +
+                         (KIND == CL_KV_INT4 && D == 64 ? 8 * (g % 2) : 0);
+  uint32_t vread[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) vread[j] = turn(4 * g + j) * ROWB + ROWB / 16 * c16;
+
+  // Row of the cache where tile t of step i starts.  A tile past the sequence's end, or without a page, is read
+  // from page 0, which is there; its keys are masked, or the rows that see them become NaN.
+  const auto row_of = [&](int i, int t, int* bad) -> int64_t {
+    const int blk = wave + kWaves * i;
+    const uint32_t at = k0 + (uint32_t)blk * kBlock + 16 * t;
+    int page = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + t);
+    if (blk >= blocks || at >= n) {
+      page = 0;
+    } else if (page < 0) {
+      page = 0;
+      *bad |= 1 << t;
+    }
+    const int tile = (int)(at >> 4) & ((1 << tiles_shift) - 1);
+    return (((int64_t)page * a.c.heads + hk) << a.page_shift) + (tile << 4);
+  };
+  // Asks for step i's block: K and V into LDS, the scales into registers.  Returns the tiles (bits) without a page.
+  const auto load = [&](int i, Scales<KIND>& x) -> int {
+    if (i > 0 && (i & 31) == 0) load_pages(k0, i);
+    int bad = 0;
+    int64_t row[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) row[t] = row_of(i, t, &bad);
+    uint8_t* const to = buf;
+    if constexpr (TILEB >= 1024) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q) {
+          load_to_lds(kb + row[t] * ROWB + kfrom[q], to + t * TILEB + 1024 * q);
+          load_to_lds(vb + row[t] * ROWB + vfrom[q], to + (2 + t) * TILEB + 1024 * q);
+        }
+    } else {
+      const int64_t mine = l < 32 ? row[0] : row[1];
+      load_to_lds(kb + mine * ROWB + kfrom[0], to);
+      load_to_lds(vb + mine * ROWB + vfrom[0], to + 2 * TILEB);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint16_t* ksp = a.c.k_scale + row[t] * SC;
+      const uint16_t* vsp = a.c.v_scale + row[t] * SC;
+      if constexpr (KIND == CL_KV_INT8) {
+        x.k[t] = *reinterpret_cast<const u2*>(ksp + 4 * g);
+        x.v[t] = *reinterpret_cast<const u2*>(vsp + 4 * g);
+      } else {
+        x.k[t] = ksp[(uint32_t)(c16 * SC + (D == 128 ? g : g / 2))];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.v[4 * t + j] = vsp[(uint32_t)((4 * g + j) * SC + CB * c16 / 32)];
+      }
+    }
+    return bad;
+  };
+
+  // ---- the first block and raw Q
+  const int steps = wave < blocks ? (blocks - wave + kWaves - 1) / kWaves : 0;
+  Scales<KIND> sc_next;
+  int bad_next = 0;
+  if (steps > 0) bad_next = load(0, sc_next);
+  u4 raw[RT][STEPS];
   int tok[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const int row = rg * ROWS + 16 * r + c16;
     tok[r] = row / G;
-    const bool there = tok[r] < n_new;
+    const bool there = tok[r] < n_new;  // otherwise the values are not used
     const uint16_t* qp = a.q + (int64_t)(first + (there ? tok[r] : 0)) * a.q_token + (int64_t)(hk * G + row % G) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) raw[r][s] = *reinterpret_cast<const u4*>(qp + q_channel<KIND, D>(s, g));
+  }
+  // ---- Q: rows n = l % 16 of each tile, scaled by a power of two, as the second operand
+  uint32_t q[RT][STEPS][4];
+  float rowc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
     float f[STEPS][8], top = 0.f;
     bool fine = true;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      u4 raw = {0, 0, 0, 0};
-      if (there) raw = *reinterpret_cast<const u4*>(qp + q_channel<KIND, D>(s, g));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint16_t e = (uint16_t)(raw[j / 2] >> (16 * (j % 2)));
+        const uint16_t e = (uint16_t)(raw[r][s][j / 2] >> (16 * (j % 2)));
         f[s][j] = a.bf16 ? Elem<CL_BF16>::up(e) : Elem<CL_F16>::up(e);
         fine = fine && fabsf(f[s][j]) < INFINITY;
         top = fmaxf(top, fabsf(f[s][j]));
@@ -203,131 +333,93 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
   }
 
   f4 o[RT][CB];
-  float m[RT], sum[RT];
+  float top[RT], m[RT], sum[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    m[r] = kNone;
+    top[r] = m[r] = kNone;
     sum[r] = 0.f;
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) o[r][cb] = f4{0.f, 0.f, 0.f, 0.f};
   }
-  float vref = 0.f;  // a power of two above every V scale seen (int8)
-  float vmul = 0.f;  // 2^kProbBits / vref
+  float vref = KIND == CL_KV_INT8 ? 0.f : 1.f;  // a power of two above every V scale seen (int4: V carries its scales)
 
-  const uint8_t* const kb = static_cast<const uint8_t*>(a.c.k);
-  const uint8_t* const vb = static_cast<const uint8_t*>(a.c.v);
-  const int tiles_shift = a.page_shift - 4;  // tiles of 16 keys in a page
-  constexpr int ROWB = KIND == CL_KV_INT8 ? D : D / 2;
-  constexpr int SC = KIND == CL_KV_INT8 ? 1 : D / 32;
-
-  // pages of the wavefront's next 64 tiles, one to a lane: -1 outside the cache or the table, 0 for a tile past
-  // the end (its keys are masked; page 0 is there to be read)
-  int pages = 0;
-  const auto load_pages = [&](int i) {
-    const int64_t at = k0 + ((int64_t)(wave + kWaves * (i + (l >> 1))) * kBlock) + 16 * (l & 1);
-    int p = 0;
-    if (at < n) {
-      const int64_t col = at >> a.page_shift;
-      p = col < a.table_width ? a.block_table[(int64_t)b * a.table_width + col] : -1;
-      if (p < 0 || p >= a.c.pages) p = -1;
-    }
-    pages = p;
-  };
-  // Loads step i's block; returns whether a tile of it has no page.
-  const auto load = [&](int i, Block<KIND, D>& x) -> int {
-    if ((i & 31) == 0) load_pages(i);
-    int bad = 0;
+  for (int i = 0; i < steps; ++i) {
+    // the block moves from LDS into registers, then the next one flies for a whole step
+    wait_loads();
+    u4 kr[2][KIND == CL_KV_INT8 ? D / 64 : 1];
+    u2 vr[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int page = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + t);
-      if (page < 0) bad |= 1 << t;
-      const int tile = (int)((k0 + (int64_t)(wave + kWaves * i) * kBlock) >> 4) + t;
-      const int64_t row = (((int64_t)max(page, 0) * a.c.heads + hk) << a.page_shift) + ((tile & ((1 << tiles_shift) - 1)) << 4);
-      const uint8_t* kp = kb + row * ROWB;
-      const uint8_t* vp = vb + row * ROWB;
-      const uint16_t* ksp = a.c.k_scale + row * SC;
-      const uint16_t* vsp = a.c.v_scale + row * SC;
-      if constexpr (KIND == CL_KV_INT8) {
-#pragma unroll
-        for (int p = 0; p < D / 64; ++p) x.k[t][p] = *reinterpret_cast<const u4*>(kp + c16 * ROWB + 64 * p + 16 * g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t* at = vp + (4 * g + j) * ROWB + CB * c16;
-          if constexpr (D == 128)
-            x.v[4 * t + j] = *reinterpret_cast<const u2*>(at);
-          else
-            x.v[4 * t + j].x = *reinterpret_cast<const uint32_t*>(at);
-        }
-        x.ks[t] = *reinterpret_cast<const u2*>(ksp + 4 * g);
-        x.vs[t] = *reinterpret_cast<const u2*>(vsp + 4 * g);
+      const uint8_t* const kt = buf + t * TILEB;
+      if constexpr (KIND == CL_KV_INT4 && D == 64) {
+        const u2 half = *reinterpret_cast<const u2*>(kt + kread);
+        kr[t][0].x = half.x, kr[t][0].y = half.y;
       } else {
-        if constexpr (D == 128) {
-          x.k[t] = *reinterpret_cast<const u4*>(kp + c16 * ROWB + 16 * g);
-        } else {
-          const u2 half = *reinterpret_cast<const u2*>(kp + c16 * ROWB + 8 * g);
-          x.k[t].x = half.x, x.k[t].y = half.y;
-        }
-        x.ks[t] = ksp[c16 * SC + (D == 128 ? g : g / 2)];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint8_t* at = vp + (4 * g + j) * ROWB + CB / 2 * c16;
-          if constexpr (D == 128)
-            x.v[4 * t + j] = *reinterpret_cast<const uint32_t*>(at);
-          else
-            x.v[4 * t + j] = *reinterpret_cast<const uint16_t*>(at);
-          x.vs[4 * t + j] = vsp[(4 * g + j) * SC + CB * c16 / 32];
-        }
+        kr[t][0] = *reinterpret_cast<const u4*>(kt + kread);
+        if constexpr (KIND == CL_KV_INT8 && D == 128) kr[t][1] = *reinterpret_cast<const u4*>(kt + (kread ^ 64));
       }
     }
-    return bad;
-  };
-
-  const int steps = wave < blocks ? (blocks - wave + kWaves - 1) / kWaves : 0;
-  Block<KIND, D> cur, nxt;
-  int bad = steps > 0 ? load(0, cur) : 0;
-  for (int i = 0; i < steps; ++i) {
-    const int bad_next = i + 1 < steps ? load(i + 1, nxt) : 0;
-    const int64_t j0 = k0 + (int64_t)(wave + kWaves * i) * kBlock;
-    const int left = (int)min(n - j0, (int64_t)kBlock);  // keys of the block that exist
-    const bool special = j0 + kBlock > ctx || bad;       // some rows may not see some keys
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t* const at = buf + (2 + j / 4) * TILEB + vread[j % 4];
+      if constexpr (KIND == CL_KV_INT8 && D == 128)
+        vr[j] = *reinterpret_cast<const u2*>(at);
+      else if constexpr (KIND == CL_KV_INT4 && D == 64)
+        vr[j].x = *reinterpret_cast<const uint16_t*>(at);
+      else
+        vr[j].x = *reinterpret_cast<const uint32_t*>(at);
+    }
+    wait_lds();
+    const Scales<KIND> sc = sc_next;
+    const int bad = bad_next;
+    if (i + 1 < steps) bad_next = load(i + 1, sc_next);
+    const uint32_t j0 = k0 + (uint32_t)(wave + kWaves * i) * kBlock;
+    const int left = (int)min(n - j0, (uint32_t)kBlock);         // keys of the block that exist
+    const bool special = j0 + kBlock > (uint32_t)ctx || bad;     // some rows may not see some keys
 
     // ---- scores
     f4 s[RT][2];
 #pragma unroll
     for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int st = 0; st < STEPS; ++st) {
         uint32_t k[4];
         if constexpr (KIND == CL_KV_INT8) {
-          const u4 raw = cur.k[t][st / 2];
+          const u4 raw = kr[t][st / 2];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             k[j] = widen8(perm(0, raw[2 * (st % 2) + j / 2], j % 2 ? 0x0C030C02u : 0x0C010C00u));
         } else {
-          const h2 ks = __builtin_bit_cast(h2, (uint32_t)cur.ks[t] * 0x10001u);
+          const h2 ks = __builtin_bit_cast(h2, (uint32_t)sc.k[t] * 0x10001u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) k[j] = widen4(cur.k[t][st], 4 * j, ks);
+          for (int j = 0; j < 4; ++j) k[j] = widen4(kr[t][0][st], 4 * j, ks);
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r][t] = mfma16(k, q[r][st], s[r][t]);
       }
-    float vs[8];
+    }
     if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int sh = 16 * (j % 2);
-        const float ks = Elem<CL_F16>::up((uint16_t)(cur.ks[j / 4][j % 4 / 2] >> sh));
-        vs[j] = Elem<CL_F16>::up((uint16_t)(cur.vs[j / 4][j % 4 / 2] >> sh));
-        const int key = 16 * (j / 4) + 4 * g + j % 4;
-        if (special && key >= left) vs[j] = 0.f;  // no token there: the scale may be anything
+        const float ks = Elem<CL_F16>::up((uint16_t)(sc.k[j / 4][j % 4 / 2] >> (16 * (j % 2))));
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r][j / 4][j % 4] *= ks;
       }
     }
+    float vs[8];
+    if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vs[j] = Elem<CL_F16>::up((uint16_t)(sc.v[j / 4][j % 4 / 2] >> (16 * (j % 2))));
+    }
     if (special) {
-      const int64_t rel = j0 - ctx;  // place of the block's first key among the new tokens
+      if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (16 * (j / 4) + 4 * g + j % 4 >= left) vs[j] = 0.f;  // no token there: the scale may be anything
+      }
+      const int64_t rel = (int64_t)j0 - ctx;  // place of the block's first key among the new tokens
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         uint32_t see;  // keys of the block that the row sees
@@ -366,7 +458,7 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
       float t = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
                       fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
       up[r] = t * rowc[r];
-      move |= up[r] > m[r] + kSlack;
+      move |= up[r] > top[r] + kSlack;
     }
     float vtop = 0.f;
     if constexpr (KIND == CL_KV_INT8) {
@@ -375,25 +467,23 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
       move |= vtop > vref;
     }
     if (__any(move)) {
-      float ratio = 1.f;
+      float to = vref;
       if constexpr (KIND == CL_KV_INT8) {
         vtop = row_max(vtop);
-        if (vtop > vref) {
-          const float to = 2.f * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, vtop) & 0x7F800000u);
-          ratio = vref / to;
-          vref = to;
-          vmul = (float)(1 << kProbBits) / to;
-        }
+        if (vtop > vref) to = 2.f * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, vtop) & 0x7F800000u);
       }
+      // m is the running maximum less log2(2^kProbBits / vref): sum and o carry that factor, which the quotient loses
+      const float lift = to > 0.f ? __builtin_amdgcn_logf(to) - kProbBits : 0.f;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const float top = fmaxf(m[r], row_max(up[r]));
-        const float old = __builtin_amdgcn_exp2f(m[r] - top);
-        m[r] = top;
+        top[r] = fmaxf(top[r], row_max(up[r]));
+        const float next = top[r] + lift, old = __builtin_amdgcn_exp2f(m[r] - next);
+        m[r] = next;
         sum[r] *= old;
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) o[r][cb] *= old * ratio;
+        for (int cb = 0; cb < CB; ++cb) o[r][cb] *= old;
       }
+      vref = to;
     }
     // ---- probabilities
     uint32_t p[RT][4];
@@ -402,10 +492,9 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
       float e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = s[r][j / 4][j % 4];
-        e[j] = __builtin_amdgcn_exp2f(x * rowc[r] - m[r]);
+        e[j] = __builtin_amdgcn_exp2f(s[r][j / 4][j % 4] * rowc[r] - m[r]);
         sum[r] += e[j];
-        e[j] *= KIND == CL_KV_INT8 ? vs[j] * vmul : (float)(1 << kProbBits);
+        if constexpr (KIND == CL_KV_INT8) e[j] *= vs[j];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -418,40 +507,39 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
         uint32_t v[4];
         const uint32_t sel = 0x0C040C00u + 0x00010001u * (cb % 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = widen8(perm(cur.v[2 * j + 1][cb / 4], cur.v[2 * j][cb / 4], sel));
+        for (int j = 0; j < 4; ++j) v[j] = widen8(perm(vr[2 * j + 1][cb / 4], vr[2 * j][cb / 4], sel));
 #pragma unroll
         for (int r = 0; r < RT; ++r) o[r][cb] = mfma16(v, p[r], o[r][cb]);
       }
     } else {
-      h2 sc[4];
+      h2 mul[4];
       uint32_t lo[4], hi[4];  // channels 0..3 and 4..7 of two keys, one in each half
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t s0 = cur.vs[2 * j], s1 = cur.vs[2 * j + 1];
+        uint32_t s0 = sc.v[2 * j], s1 = sc.v[2 * j + 1];
         if (special) {  // no token there: the scale may be anything
           const int key = 16 * (j / 2) + 4 * g + 2 * (j % 2);
           if (key >= left) s0 = 0;
           if (key + 1 >= left) s1 = 0;
         }
-        sc[j] = __builtin_bit_cast(h2, s0 | s1 << 16);
-        lo[j] = perm(cur.v[2 * j + 1], cur.v[2 * j], 0x05040100u);
-        hi[j] = perm(cur.v[2 * j + 1], cur.v[2 * j], 0x07060302u);
+        mul[j] = __builtin_bit_cast(h2, s0 | s1 << 16);
+        lo[j] = perm(vr[2 * j + 1].x, vr[2 * j].x, 0x05040100u);
+        hi[j] = perm(vr[2 * j + 1].x, vr[2 * j].x, 0x07060302u);
       }
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) {
         uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = widen4(cb < 4 ? lo[j] : hi[j], 4 * (cb % 4), sc[j]);
+        for (int j = 0; j < 4; ++j) v[j] = widen4(cb < 4 ? lo[j] : hi[j], 4 * (cb % 4), mul[j]);
 #pragma unroll
         for (int r = 0; r < RT; ++r) o[r][cb] = mfma16(v, p[r], o[r][cb]);
       }
     }
-    cur = nxt;
-    bad = bad_next;
   }
 
   // ---- join the four wavefronts
-  const float unit = KIND == CL_KV_INT8 ? 512.f / (float)(1 << kProbBits) * vref : 1.f / (float)(1 << kProbBits);
+  __syncthreads();  // the blocks' memory becomes the outputs'
+  constexpr float unit = KIND == CL_KV_INT8 ? 512.f : 1.f;  // codes entered as code * 2^-9
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const float l_row = row_sum(sum[r]);
@@ -491,7 +579,7 @@ __global__ void __launch_bounds__(256) tree_attention_kernel(AttnArgs a) {
     if (splits == 1) {
       store(row, x, den == 0.f ? 0.f : 1.f / den);
     } else {
-      const int64_t at = (cell * gridDim.x + split) * ROWS + row;
+      const int64_t at = (cell * gridDim.z + split) * ROWS + row;
       if (ch == 0) a.part_ml[at] = make_float2(top, den);
       f4* po = reinterpret_cast<f4*>(a.part_o + at * D + ch);
       po[0] = f4{x[0], x[1], x[2], x[3]};
@@ -511,7 +599,7 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, in
   __shared__ float s_red[2 * kWaves];
   const int tid = threadIdx.x, cell = blockIdx.x, row = blockIdx.y;
   const int rg = cell % a.row_groups, hk = cell / a.row_groups % a.c.heads, b = cell / a.row_groups / a.c.heads;
-  const Range x = range_of(a, b, max_splits);
+  const Range x = range_of(a, a.cu_q[b], a.cu_q[b + 1], a.ctx_lens[b], max_splits);
   const int G = a.group, at = rg * a.rows_per_group + row;
   if (x.splits < 2 || at >= x.n_new * G) return;
   const int64_t base = (int64_t)cell * max_splits * a.rows_per_group + row;
@@ -569,9 +657,13 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   p.row_groups = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
   p.cells = sequences * heads * p.row_groups;
   const int64_t keys = max_ctx + max_q, unit = kBlock * kWaves;
-  int64_t splits = (1024 + p.cells - 1) / p.cells;
+  // two workgroups to a CU where there are fewer cells; chunks of at most kMaxChunk, so that one long sequence among
+  // short ones does not run alone at the end
+  int64_t splits = (512 + p.cells - 1) / p.cells;
+  if (splits < (keys + kMaxChunk - 1) / kMaxChunk) splits = (keys + kMaxChunk - 1) / kMaxChunk;
   const int64_t most = (keys + unit - 1) / unit;
   if (splits > most) splits = most;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   p.chunk = (int)((((keys + splits - 1) / splits) + unit - 1) / unit * unit);
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
   const size_t parts = p.splits > 1 ? (size_t)p.cells * p.splits * 16 * p.rt : 0;
@@ -583,7 +675,9 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
 
 template <int KIND, int D>
 void launch(const AttnPlan& p, const AttnArgs& a, int sequences, hipStream_t s) {
-  const dim3 grid(p.splits, a.c.heads * p.row_groups, sequences);
+  // Chunks vary slowest: workgroups go to the eight XCDs in turn, and the last chunks of a ragged batch are mostly
+  // empty.  Row groups of a head, which read the same keys, meet on one XCD where heads are a multiple of 8.
+  const dim3 grid(a.c.heads * p.row_groups, sequences, p.splits);
   if (p.rt == 1)
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1>), grid, dim3(256), 0, s, a);
   else
