@@ -13,15 +13,14 @@
 // inserted one by one.  A tile first raises that bar to the top_k-th largest of its
 // lanes' maxima, which bounds the insertions whatever the order of the row.
 //
-// Bound by the read of the logits.
+// Bound by the read of the logits where there are rows for the whole card; a single
+// row by one CU's share of it and the latency of the joins.
 #include "serving.h"
 
 namespace cl {
 namespace {
 
-constexpr int kThreads = 256, kLpWaves = kThreads / 64;
-constexpr int kPer = 32;                  // logits of a thread's tile
-constexpr int kTile = kThreads * kPer;    // logits of a workgroup's tile
+constexpr int kPer = 32;  // logits of a thread's tile
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 
 typedef unsigned long long u64;
@@ -34,9 +33,7 @@ struct LogprobArgs {
   float* entropy;
   int32_t* top_ids;
   float* top_logp;
-  float4* part;   // [rows, parts] (m, l, w, -)
-  u64* part_top;  // [rows, parts, top_k]
-  int vocab, given, top_k, parts, span;  // span: logits of a part
+  int vocab, given, top_k;
 };
 
 // Order of the alternatives as one number: larger logits first (-0 as +0, NaN largest), then lower ids.
@@ -105,14 +102,15 @@ struct Best {
   }
 };
 
-// One part of a row: its logits [j0, j1).
-template <int DT, bool VEC>
-__device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ x, int j0, int j1, Stat& st, Best& best) {
+// A row's logits [0, j1), by a workgroup of kThreads.
+template <int DT, bool VEC, int kThreads>
+__device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ x, int j1, Stat& st, Best& best) {
+  constexpr int kTile = kThreads * kPer;
   typedef typename Elem<DT>::raw raw;
   constexpr int V = VEC ? 16 / (int)sizeof(raw) : 1;  // logits of a load
   const int tid = threadIdx.x;
   st = Stat{-INFINITY, 0.f, 0.f};
-  for (int t0 = j0; t0 < j1; t0 += kTile) {
+  for (int t0 = 0; t0 < j1; t0 += kTile) {
     float v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer / V; ++i) {
@@ -180,6 +178,7 @@ __device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ 
 }
 
 // Joins the workgroup's wavefronts; the result is in wavefront 0 (st in all its lanes).
+template <int kLpWaves>
 __device__ __forceinline__ void join_waves(Stat& st, Best& best) {
   __shared__ float s_st[kLpWaves][3];
   __shared__ u64 s_top[kLpWaves][32];
@@ -189,9 +188,13 @@ __device__ __forceinline__ void join_waves(Stat& st, Best& best) {
   if (lane < best.k) s_top[wave][lane] = best.key;
   __syncthreads();
   if (wave) return;
-  for (int v = 1; v < kLpWaves; ++v) {
-    join(st, Stat{s_st[v][0], s_st[v][1], s_st[v][2]});
-    if (best.k) best.insert(lane < best.k ? s_top[v][lane] : 0, best.k == 64 ? ~0ull : (1ull << best.k) - 1);
+  // the wavefronts' sums one to a lane, then their keys 64 at a time
+  st = lane < kLpWaves ? Stat{s_st[lane][0], s_st[lane][1], s_st[lane][2]} : Stat{-INFINITY, 0.f, 0.f};
+  join_lanes(st);
+  const int keys = (kLpWaves - 1) * best.k;
+  for (int k0 = 0; k0 < keys; k0 += 64) {
+    const int i = k0 + lane;
+    best.insert(i < keys ? s_top[1 + i / best.k][i % best.k] : 0, ~0ull);
   }
 }
 
@@ -213,71 +216,34 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, int t, const typena
   }
 }
 
-template <int DT, bool VEC>
+// One workgroup a row.
+template <int DT, bool VEC, int kThreads>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
-  const int part = blockIdx.x % a.parts, t = blockIdx.x / a.parts;
+  const int t = blockIdx.x;
   const auto* x = static_cast<const typename Elem<DT>::raw*>(a.x) + t * a.x_row;
   Stat st;
   Best best;
   best.clear(a.top_k);
-  const int j0 = part * a.span;
-  scan<DT, VEC>(x, j0, min(j0 + a.span, a.vocab), st, best);
-  join_waves(st, best);
-  if (threadIdx.x >= 64) return;
-  if (a.parts == 1) {
-    finish<DT>(a, t, x, st, best);
-  } else {
-    if (threadIdx.x == 0) a.part[blockIdx.x] = make_float4(st.m, st.l, st.w, 0.f);
-    if ((int)threadIdx.x < a.top_k) a.part_top[(int64_t)blockIdx.x * a.top_k + threadIdx.x] = best.key;
-  }
+  scan<DT, VEC, kThreads>(x, a.vocab, st, best);
+  join_waves<kThreads / 64>(st, best);
+  if (threadIdx.x < 64) finish<DT>(a, t, x, st, best);
 }
 
-// Joins a row's parts: one wavefront a row.
-template <int DT>
-__global__ void __launch_bounds__(64) logprobs_join_kernel(LogprobArgs a) {
-  const int t = blockIdx.x, lane = threadIdx.x;
-  Stat st = {-INFINITY, 0.f, 0.f};
-  Best best;
-  best.clear(a.top_k);
-  for (int p = lane; p < a.parts; p += 64) {
-    const float4 v = a.part[(int64_t)t * a.parts + p];
-    join(st, Stat{v.x, v.y, v.z});
-  }
-  join_lanes(st);
-  const int keys = a.parts * a.top_k;
-  for (int k0 = 0; k0 < keys; k0 += 64) {
-    const int k = k0 + lane;
-    best.insert(k < keys ? a.part_top[(int64_t)t * keys + k] : 0, ~0ull);
-  }
-  finish<DT>(a, t, static_cast<const typename Elem<DT>::raw*>(a.x) + t * a.x_row, st, best);
-}
-
-// Parts of a row: one where the rows fill the card, otherwise parts of at least 2048 logits.
-struct LogprobPlan {
-  int parts, span;
-  size_t stat_bytes, need;
-};
-LogprobPlan plan_logprobs(int64_t rows, int vocab, int top_k) {
-  LogprobPlan p;
-  int64_t parts = (1024 + rows - 1) / rows;
-  const int64_t most = (vocab + 2047) / 2048;
-  if (rows >= 512) parts = 1;
-  if (parts > most) parts = most;
-  p.span = (int)((vocab + parts - 1) / parts + 15) / 16 * 16;
-  p.parts = (vocab + p.span - 1) / p.span;
-  p.stat_bytes = p.parts > 1 ? (size_t)rows * p.parts * sizeof(float4) : 0;
-  p.need = p.parts > 1 ? p.stat_bytes + (size_t)rows * p.parts * top_k * sizeof(u64) : 0;
-  return p;
+template <int DT, int kThreads>
+void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
+  if (vec)
+    hipLaunchKernelGGL((logprobs_kernel<DT, true, kThreads>), dim3(rows), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((logprobs_kernel<DT, false, kThreads>), dim3(rows), dim3(kThreads), 0, s, a);
 }
 
 template <int DT>
 void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
-  const dim3 grid((unsigned)rows * a.parts);
-  if (vec)
-    hipLaunchKernelGGL((logprobs_kernel<DT, true>), grid, dim3(kThreads), 0, s, a);
+  // four wavefronts a row where the rows fill the card, sixteen where they do not
+  if (rows >= 512)
+    launch_logprobs<DT, 256>(a, rows, vec, s);
   else
-    hipLaunchKernelGGL((logprobs_kernel<DT, false>), grid, dim3(kThreads), 0, s, a);
-  if (a.parts > 1) hipLaunchKernelGGL((logprobs_join_kernel<DT>), dim3(rows), dim3(64), 0, s, a);
+    launch_logprobs<DT, 1024>(a, rows, vec, s);
 }
 
 }  // namespace
@@ -285,14 +251,9 @@ void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
 
 using namespace cl;
 
-extern "C" size_t cl_token_logprobs_work_bytes(int32_t rows, int32_t vocab, int32_t top_k) {
-  if (rows < 1 || vocab < 1 || top_k < 0) return 0;
-  return plan_logprobs(rows, vocab, top_k).need;
-}
-
 extern "C" cl_status cl_token_logprobs(const void* x, int32_t dtype, int64_t x_row, int32_t rows, int32_t vocab,
                                        const int32_t* ids, int32_t given, float* logp, float* entropy, int32_t top_k,
-                                       int32_t* top_ids, float* top_logp, void* work, size_t work_bytes, void* stream) {
+                                       int32_t* top_ids, float* top_logp, void* stream) {
   clear_error();
   if (rows < 0 || vocab < 1 || given < 0 || top_k < 0) return fail(CL_EINVAL, "logprobs: a size is out of range");
   if (!elem_ok(dtype)) return fail(CL_EINVAL, "logprobs: unknown element type");
@@ -303,15 +264,8 @@ extern "C" cl_status cl_token_logprobs(const void* x, int32_t dtype, int64_t x_r
   if (!x || !entropy || (given && (!ids || !logp)) || (top_k && (!top_ids || !top_logp)))
     return fail(CL_EINVAL, "logprobs: a required pointer is NULL");
   if (!aligned_to(x, elem_size(dtype))) return fail(CL_EINVAL, "logprobs: x is misaligned for its type");
-  const LogprobPlan p = plan_logprobs(rows, vocab, top_k);
-  if ((int64_t)rows * p.parts > 0x7FFFFFFF) return fail(CL_ESIZE, "logprobs: too many rows");
-  if (p.need && (!work || work_bytes < p.need))
-    return fail(CL_ENOMEM, "logprobs: work has %zu bytes, %zu are needed", work_bytes, p.need);
-  if (!aligned_to(work, 16)) return fail(CL_EINVAL, "logprobs: work must be 16-byte aligned");
-  const LogprobArgs a = {x, x_row, ids, logp, entropy, top_ids, top_logp, static_cast<float4*>(work),
-                         reinterpret_cast<u64*>(static_cast<uint8_t*>(work) + p.stat_bytes), vocab, given, top_k, p.parts,
-                         p.span};
-  // 16-byte loads where every row starts on a 16-byte boundary (parts do, as spans are multiples of 16)
+  const LogprobArgs a = {x, x_row, ids, logp, entropy, top_ids, top_logp, vocab, given, top_k};
+  // 16-byte loads where every row starts on a 16-byte boundary
   const bool vec = aligned_to(x, 16) && (x_row * (int64_t)elem_size(dtype)) % 16 == 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)

@@ -26,8 +26,9 @@
 // wavefront a step), so that the output is rarely rescaled.
 //
 // The keys of a sequence are cut into chunks, a workgroup each, whose four
-// wavefronts take every fourth block of 32 keys; the partial outputs of more than one
-// chunk are joined by a second, small launch.
+// wavefronts take every fourth block of 32 keys; the partial outputs of a few
+// chunks are joined by the workgroup that finishes last, those of many by a second,
+// small launch, in either case in chunk order.
 #include "serving.h"
 #include "unpack.h"
 
@@ -47,7 +48,12 @@ constexpr float kSlack = 4.f;      // log2 by which a score may pass the running
 constexpr int kProbBits = 11;      // probabilities are scaled by 2^11: with the slack at most 2^15
 
 constexpr int kMaxChunk = 2048;    // keys of a workgroup
+constexpr int kInline = 8;         // chunks that the last workgroup of a cell joins; more are joined by a launch
+constexpr int kMaxCells = 65536;   // cells (sequence, kv head, row group) that may be joined so: their counters open the workspace
 constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
+
+constexpr size_t kCounterBytes = kMaxCells * sizeof(uint32_t);
+static_assert(kCounterBytes == CL_ATTENTION_COUNTER_BYTES, "the header's figure");
 
 struct AttnArgs {
   const uint16_t* q;
@@ -57,6 +63,7 @@ struct AttnArgs {
   const int32_t* ctx_lens;
   const int32_t* cu_q;
   const uint64_t* mask;
+  uint32_t* counters;  // NULL: the join is a launch of its own
   float2* part_ml;
   float* part_o;
   int64_t q_token, q_head;
@@ -148,6 +155,17 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
                                    16, 0, 2);
 }
 
+// Device-scope (all XCDs) accesses of two floats.
+__device__ __forceinline__ void store_dev2(float2* p, float x, float y) {
+  const uint64_t v = (uint64_t)__builtin_bit_cast(uint32_t, y) << 32 | __builtin_bit_cast(uint32_t, x);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 load_dev2(const float2* p) {
+  const uint64_t v = __hip_atomic_load(const_cast<uint64_t*>(reinterpret_cast<const uint64_t*>(p)), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__builtin_bit_cast(float, (uint32_t)v), __builtin_bit_cast(float, (uint32_t)(v >> 32)));
+}
+
 // Waits for every load asked for so far, those into LDS among them.
 __device__ __forceinline__ void wait_loads() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -176,6 +194,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   __shared__ __align__(1024) uint8_t s_mem[KVBYTES > OBYTES ? KVBYTES : OBYTES];
   float (*const s_o)[ROWS][STRIDE] = reinterpret_cast<float (*)[ROWS][STRIDE]>(s_mem);
   __shared__ float2 s_ml[kWaves][ROWS];
+  __shared__ int s_last;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, c16 = l & 15, g = l >> 4;
   const int b = blockIdx.y, hk = blockIdx.x % a.c.heads, rg = blockIdx.x / a.c.heads;
@@ -580,17 +599,52 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
       store(row, x, den == 0.f ? 0.f : 1.f / den);
     } else {
       const int64_t at = (cell * gridDim.z + split) * ROWS + row;
-      if (ch == 0) a.part_ml[at] = make_float2(top, den);
-      f4* po = reinterpret_cast<f4*>(a.part_o + at * D + ch);
-      po[0] = f4{x[0], x[1], x[2], x[3]};
-      po[1] = f4{x[4], x[5], x[6], x[7]};
+      if (ch == 0) store_dev2(a.part_ml + at, top, den);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) store_dev2(reinterpret_cast<float2*>(a.part_o + at * D + ch + j), x[j], x[j + 1]);
     }
+  }
+  if (splits == 1 || !a.counters) return;
+  // ---- few chunks: the workgroup that comes last joins them
+  wait_stores();
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t before = __hip_atomic_fetch_add(&a.counters[cell], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = before == (uint32_t)splits - 1;
+    if (s_last) __hip_atomic_store(&a.counters[cell], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!s_last) return;
+  for (int row = tid / PARTS; row < rows; row += 256 / PARTS) {
+    float mv[kInline], lv[kInline], x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, top = kNone, den = 0.f;
+    float2 part[kInline][4];
+#pragma unroll
+    for (int v = 0; v < kInline; ++v) {
+      const int64_t at = (cell * gridDim.z + min(v, splits - 1)) * ROWS + row;
+      const float2 ml = load_dev2(a.part_ml + at);
+      mv[v] = v < splits ? ml.x : kNone;
+      lv[v] = v < splits ? ml.y : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[v][j] = load_dev2(reinterpret_cast<const float2*>(a.part_o + at * D + ch + 2 * j));
+    }
+#pragma unroll
+    for (int v = 0; v < kInline; ++v) top = fmaxf(top, mv[v]);
+#pragma unroll
+    for (int v = 0; v < kInline; ++v) {
+      const float w = v < splits ? __builtin_amdgcn_exp2f(mv[v] - top) : 0.f;
+      den += w * lv[v];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (v < splits) x[2 * j] += w * part[v][j].x, x[2 * j + 1] += w * part[v][j].y;
+      }
+    }
+    store(row, x, den == 0.f ? 0.f : 1.f / den);
   }
 }
 
 // Joins the partial outputs of a row's chunks, in chunk order within each of eight strands and the strands in
-// order: 32 lanes (dim 128) or 16 hold four channels each.  A launch of its own rather than the workgroup that
-// finishes last: rows x chunks partials are read by as many workgroups as there are rows.
+// order: 32 lanes (dim 128) or 16 hold four channels each.  For more than kInline chunks this launch of its own, where
+// as many workgroups as there are rows read the partials, beats one workgroup that reads them all.
 template <int D>
 __global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, int max_splits) {
   constexpr int LANES = D / 4, STRANDS = 256 / LANES;
@@ -647,6 +701,7 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, in
 struct AttnPlan {
   int rt, row_groups, splits, chunk;
   int64_t cells;
+  bool joined_inline;
   size_t ml_bytes, o_bytes, need;
 };
 
@@ -669,7 +724,8 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   const size_t parts = p.splits > 1 ? (size_t)p.cells * p.splits * 16 * p.rt : 0;
   p.ml_bytes = parts * sizeof(float2);
   p.o_bytes = parts * dim * sizeof(float);
-  p.need = p.ml_bytes + p.o_bytes;
+  p.joined_inline = p.splits > 1 && p.splits <= kInline && p.cells <= kMaxCells;
+  p.need = parts ? kCounterBytes + p.ml_bytes + p.o_bytes : 0;
   return p;
 }
 
@@ -682,7 +738,7 @@ void launch(const AttnPlan& p, const AttnArgs& a, int sequences, hipStream_t s) 
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 2>), grid, dim3(256), 0, s, a);
-  if (p.splits > 1)
+  if (p.splits > 1 && !p.joined_inline)
     hipLaunchKernelGGL((tree_attention_join_kernel<D>), dim3((unsigned)p.cells, 16 * p.rt), dim3(256), 0, s, a, p.splits);
 }
 
@@ -728,8 +784,9 @@ extern "C" cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_t
   if (!aligned_to(work, 16)) return fail(CL_EINVAL, "attention: work must be 16-byte aligned");
   uint8_t* w = static_cast<uint8_t*>(work);
   AttnArgs a = {static_cast<const uint16_t*>(q), static_cast<uint16_t*>(o), *cache, block_table, ctx_lens, cu_q,
-                reinterpret_cast<const uint64_t*>(mask), reinterpret_cast<float2*>(w),
-                reinterpret_cast<float*>(w + p.ml_bytes),
+                reinterpret_cast<const uint64_t*>(mask), p.joined_inline ? reinterpret_cast<uint32_t*>(w) : nullptr,
+                reinterpret_cast<float2*>(w + kCounterBytes),
+                reinterpret_cast<float*>(w + kCounterBytes + p.ml_bytes),
                 q_token, q_head, tokens, q_heads / cache->heads, table_width, max_q, mask_words, dtype == CL_BF16,
                 p.chunk, p.row_groups, 16 * p.rt, __builtin_ctz(cache->page_size), scale};
   hipStream_t s = static_cast<hipStream_t>(stream);

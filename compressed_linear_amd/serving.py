@@ -11,11 +11,12 @@ import ctypes
 from typing import Optional
 
 SERVING_SYMBOLS = ["cl_rope_table", "cl_rope", "cl_kv_append", "cl_kv_read", "cl_tree_attention_work_bytes",
-                   "cl_tree_attention", "cl_token_logprobs_work_bytes", "cl_token_logprobs"]
+                   "cl_tree_attention", "cl_token_logprobs"]
 
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 KV_KIND = {"int8": 0, "int4": 1}
+COUNTER_BYTES = 262144  # CL_ATTENTION_COUNTER_BYTES
 
 
 class cl_kv_cache(ctypes.Structure):
@@ -36,27 +37,31 @@ def declare(L):
     L.cl_tree_attention_work_bytes.argtypes = [i] * 6
     L.cl_tree_attention.argtypes = [p, i, q, q, i, i, cache, p, i, i, p, p, i, i, p, i, ctypes.c_float, p, p,
                                     ctypes.c_size_t, p]
-    L.cl_token_logprobs_work_bytes.argtypes = [i] * 3
-    L.cl_token_logprobs.argtypes = [p, i, q, i, i, p, i, p, p, i, p, p, p, ctypes.c_size_t, p]
+    L.cl_token_logprobs.argtypes = [p, i, q, i, i, p, i, p, p, i, p, p, p]
     for name in SERVING_SYMBOLS:
         getattr(L, name).restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
 
 
 _torch = None
 _lib = None
+_empty = _current_device = _raw_stream = _i32 = None
 _DT: dict = {}
 
 
 def _setup():
     """torch and the library, loaded at the first call (importing the package needs neither)."""
-    global _torch, _lib
+    global _torch, _lib, _empty, _current_device, _raw_stream, _i32
     if _lib is None:
         import torch
 
         from . import lib
-        _lib = lib()
+        _torch, _empty, _i32 = torch, torch.empty, torch.int32
+        _current_device = torch.cuda.current_device
+        # the stream's address without a Stream object around it (1.8 us of a call) where torch has that
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
         _DT.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
-        _torch = torch
+        _lib = lib()
     return _lib
 
 
@@ -68,14 +73,15 @@ def _check(st: int, where: str):
 
 def _stream(dev):
     """torch's current stream on `dev`; the library launches on the current device, so that has to be it."""
-    if dev.index != _torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is cuda:{_torch.cuda.current_device()}")
-    return _torch.cuda.current_stream(dev).cuda_stream
+    index = dev.index
+    if index != _current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{_current_device()}")
+    return _raw_stream(index)
 
 
 def _index(t, n, dev, what):
     """The address of an int32 tensor of n elements on `dev`."""
-    if t.dtype != _torch.int32 or t.device != dev or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _i32 or t.numel() != n or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 tensor of {n} elements on {dev}")
     return t.data_ptr()
 
@@ -88,10 +94,11 @@ def _heads3(x, what):
 
 
 def _table(table, dev):
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != _torch.float32 or table.device != dev \
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2 or table.dtype is not _torch.float32 or table.device != dev \
             or not table.is_contiguous():
         raise ValueError(f"table must be a contiguous float32 [positions, rot / 2, 2] tensor on {dev} (see rope_table)")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+    return table.data_ptr(), shape[0], 2 * shape[1]
 
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -118,19 +125,23 @@ def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None):
     contiguous tensor of `out_dtype` (x's type by default).  `out` may be x."""
     L = _lib or _setup()
     x = _heads3(x, "x")
-    dev = x.device
-    T, H, D = x.shape
+    dev, shape = x.device, x.shape
+    T, H, D = shape
+    xt, xh, _ = x.stride()
     if out is None:
-        out = _torch.empty((T, H, D), dtype=out_dtype or x.dtype, device=dev)
-    elif out.shape != x.shape or out.device != dev or out.stride(2) != 1 or (out_dtype or out.dtype) != out.dtype:
-        raise ValueError(f"out must be a {tuple(x.shape)} tensor on {dev} with contiguous channels")
+        out = _empty(shape, dtype=out_dtype or x.dtype, device=dev)
+        yt, yh = H * D, D
+    else:
+        yt, yh, one = out.stride() if out.dim() == 3 else (0, 0, 0)
+        if out.shape != shape or out.device != dev or one != 1 or (out_dtype or out.dtype) != out.dtype:
+            raise ValueError(f"out must be a {tuple(shape)} tensor on {dev} with contiguous channels")
     if out.dtype not in _DT:
         raise ValueError("the output must be float16, bfloat16 or float32")
     tp, rows, rot = _table(table, dev)
-    st = L.cl_rope(x.data_ptr(), _DT[x.dtype], x.stride(0), x.stride(1), T, H, D,
-                   _index(positions, T, dev, "positions"), tp, rows, rot, ROPE_LAYOUT[layout], out.data_ptr(),
-                   _DT[out.dtype], out.stride(0), out.stride(1), _stream(dev))
-    _check(st, "cl_rope")
+    st = L.cl_rope(x.data_ptr(), _DT[x.dtype], xt, xh, T, H, D, _index(positions, T, dev, "positions"), tp, rows, rot,
+                   ROPE_LAYOUT[layout], out.data_ptr(), _DT[out.dtype], yt, yh, _stream(dev))
+    if st:
+        _check(st, "cl_rope")
     return out
 
 
@@ -177,7 +188,7 @@ class KVCache:
         self._desc = cl_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page_size,
                                  heads, dim, KV_KIND[kind], 0)
         self._ref = ctypes.byref(self._desc)
-        self._work = None
+        self._work, self._work_ptr, self._work_bytes = None, None, 0
         self._outgrown: list = []
 
     def append(self, k, v, slots, positions=None, table=None, layout: str = "half"):
@@ -185,10 +196,11 @@ class KVCache:
         cache, -1 say, stores nothing).  With `table` (and int32 `positions`) the keys are rotated on
         the way, from unrounded results, as `rope` would."""
         k, v, dev = _heads3(k, "k"), _heads3(v, "v"), self.device
-        if k.shape != v.shape or k.dtype != v.dtype or k.device != dev or v.device != dev \
-                or k.shape[1] != self.heads or k.shape[2] != self.dim:
+        shape, dt = k.shape, k.dtype
+        if v.shape != shape or v.dtype is not dt or k.device != dev or v.device != dev \
+                or shape[1] != self.heads or shape[2] != self.dim:
             raise ValueError(f"k and v must be [tokens, {self.heads}, {self.dim}] of one type on {dev}")
-        T = k.shape[0]
+        T = shape[0]
         pp = tp = None
         rows = rot = 0
         if table is not None:
@@ -196,10 +208,12 @@ class KVCache:
             if positions is None:
                 raise ValueError("a table needs positions")
             pp = _index(positions, T, dev, "positions")
-        st = _lib.cl_kv_append(self._ref, k.data_ptr(), v.data_ptr(), _DT[k.dtype], T, k.stride(0), k.stride(1),
-                               v.stride(0), v.stride(1), _index(slots, T, dev, "slots"), pp, tp, rows, rot,
-                               ROPE_LAYOUT[layout], _stream(dev))
-        _check(st, "cl_kv_append")
+        kt, kh, _ = k.stride()
+        vt, vh, _ = v.stride()
+        st = _lib.cl_kv_append(self._ref, k.data_ptr(), v.data_ptr(), _DT[dt], T, kt, kh, vt, vh,
+                               _index(slots, T, dev, "slots"), pp, tp, rows, rot, ROPE_LAYOUT[layout], _stream(dev))
+        if st:
+            _check(st, "cl_kv_append")
 
     def read(self, slots, dtype=None):
         """The stored keys and values of `slots` (int32 [n]): two tensors [n, heads, dim] of `dtype` (float16
@@ -209,22 +223,24 @@ class KVCache:
         if dtype not in _DT:
             raise ValueError("dtype must be float16, bfloat16 or float32")
         n = slots.numel()
-        k = _torch.empty((n, self.heads, self.dim), dtype=dtype, device=dev)
-        v = _torch.empty((n, self.heads, self.dim), dtype=dtype, device=dev)
+        k, v = _empty((2, n, self.heads, self.dim), dtype=dtype, device=dev).unbind(0)
         st = _lib.cl_kv_read(self._ref, _index(slots, n, dev, "slots"), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
                              _stream(dev))
-        _check(st, "cl_kv_read")
+        if st:
+            _check(st, "cl_kv_read")
         return k, v
 
     def _workspace(self, sizes):
-        """The workspace for these sizes.  One that was outgrown is kept: work on another stream or a
-        recorded graph may still use it."""
+        """The attention's workspace for these sizes.  One that was outgrown is kept: work on another stream or
+        a recorded graph may still use it."""
         need = _lib.cl_tree_attention_work_bytes(*sizes)
-        if need and (self._work is None or self._work.numel() < need):
+        if need > self._work_bytes:
             if self._work is not None:
                 self._outgrown.append(self._work)
-            self._work = _torch.empty(2 * need, dtype=_torch.uint8, device=self.device)
-        return self._work
+            self._work_bytes = 2 * need
+            self._work = _empty(self._work_bytes, dtype=_torch.uint8, device=self.device)
+            self._work[:COUNTER_BYTES].zero_()  # the calls leave them so
+            self._work_ptr = self._work.data_ptr()
 
 
 def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, max_ctx: Optional[int] = None,
@@ -240,38 +256,42 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
     block table holds).  Returns [tokens, q_heads, dim] of q's type."""
     L = _lib or _setup()
     dev = cache.device
-    if q.dim() != 3 or q.device != dev or q.shape[2] != cache.dim or _DT.get(q.dtype, 2) == 2:
+    shape, dt = q.shape, _DT.get(q.dtype, 2)
+    if len(shape) != 3 or q.device != dev or shape[2] != cache.dim or dt == 2:
         raise ValueError(f"q must be a float16 or bfloat16 [tokens, q_heads, {cache.dim}] tensor on {dev}")
-    if q.stride(2) != 1 or q.stride(0) % 8 or q.stride(1) % 8 or q.data_ptr() % 16:
+    qt, qh, one = q.stride()
+    qp = q.data_ptr()
+    if one != 1 or qt % 8 or qh % 8 or qp % 16:
         q = q.contiguous()
-    T, H, D = q.shape
+        qt, qh, _ = q.stride()
+        qp = q.data_ptr()
+    T, H, D = shape
     B = ctx_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, width]")
     width = block_table.shape[1]
     words, mp = 0, None
     if tree_mask is not None:
-        if tree_mask.dim() != 2 or tree_mask.dtype != _torch.int64 or tree_mask.device != dev \
+        if tree_mask.dim() != 2 or tree_mask.dtype is not _torch.int64 or tree_mask.device != dev \
                 or tree_mask.shape[0] != T or not tree_mask.is_contiguous():
             raise ValueError(f"tree_mask must be a contiguous int64 [{T}, words] tensor on {dev}")
         words, mp = tree_mask.shape[1], tree_mask.data_ptr()
     if out is None:
-        out = _torch.empty((T, H, D), dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+        out = _empty(shape, dtype=q.dtype, device=dev)
+    elif out.shape != shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and type")
     if max_ctx is None:
         max_ctx = width * cache.page_size
-    args = (q.data_ptr(), _DT[q.dtype], q.stride(0), q.stride(1), T, H, cache._ref,
-            _index(block_table, B * width, dev, "block_table"), width, B, _index(ctx_lens, B, dev, "ctx_lens"),
-            _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
+    args = (qp, dt, qt, qh, T, H, cache._ref, _index(block_table, B * width, dev, "block_table"), width, B,
+            _index(ctx_lens, B, dev, "ctx_lens"), _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
             1.0 / D ** 0.5 if scale is None else scale, out.data_ptr())
-    work = cache._work
-    st = L.cl_tree_attention(*args, None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
-                             _stream(dev))
+    stream = _stream(dev)
+    st = L.cl_tree_attention(*args, cache._work_ptr, cache._work_bytes, stream)
     if st == -3:  # the workspace is too small for these sizes: make a larger one, once
-        work = cache._workspace((B, H, cache.heads, D, max_q, max_ctx))
-        st = L.cl_tree_attention(*args, work.data_ptr(), work.numel(), _stream(dev))
-    _check(st, "cl_tree_attention")
+        cache._workspace((B, H, cache.heads, D, max_q, max_ctx))
+        st = L.cl_tree_attention(*args, cache._work_ptr, cache._work_bytes, stream)
+    if st:
+        _check(st, "cl_tree_attention")
     return out
 
 
@@ -281,28 +301,28 @@ def token_logprobs(logits, ids, top_k: int = 0):
     (at most 32), top_ids int32 [rows, top_k] and top_logp float32 [rows, top_k]: the largest logits first,
     equal ones by the lower id.  An id outside the vocabulary gives NaN."""
     L = _lib or _setup()
-    if logits.dim() != 2 or logits.dtype not in _DT or not logits.is_cuda:
+    shape, dt = logits.shape, _DT.get(logits.dtype)
+    if len(shape) != 2 or dt is None or not logits.is_cuda:
         raise ValueError("logits must be a float16, bfloat16 or float32 [rows, vocab] tensor on a ROCm device")
-    if logits.stride(1) != 1:
+    row, one = logits.stride()
+    if one != 1:
         logits = logits.contiguous()
+        row = logits.stride(0)
     dev = logits.device
-    T, V = logits.shape
+    T, V = shape
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError(f"ids must be int32 [{T}, given]")
     C = ids.shape[1]
     ip = _index(ids, T * C, dev, "ids")
-    # one allocation holds the float outputs
-    buf = _torch.empty(T * (C + 1 + top_k), dtype=_torch.float32, device=dev)
-    logp, entropy = buf[:T * C].view(T, C), buf[T * C:T * (C + 1)]
-    top_ids = top_logp = None
-    if top_k:
-        top_ids = _torch.empty((T, top_k), dtype=_torch.int32, device=dev)
-        top_logp = buf[T * (C + 1):].view(T, top_k)
-    need = L.cl_token_logprobs_work_bytes(T, V, top_k)
-    work = _torch.empty(need, dtype=_torch.uint8, device=dev) if need else None
-    st = L.cl_token_logprobs(logits.data_ptr(), _DT[logits.dtype], logits.stride(0), T, V, ip, C, logp.data_ptr(),
-                             entropy.data_ptr(), top_k, None if top_ids is None else top_ids.data_ptr(),
-                             None if top_logp is None else top_logp.data_ptr(),
-                             None if work is None else work.data_ptr(), need, _stream(dev))
-    _check(st, "cl_token_logprobs")
+    logp = _empty((T, C), dtype=_torch.float32, device=dev)
+    entropy = _empty((T,), dtype=_torch.float32, device=dev)
+    top_ids = top_logp = tip = tlp = None
+    if top_k > 0:
+        top_ids = _empty((T, top_k), dtype=_i32, device=dev)
+        top_logp = _empty((T, top_k), dtype=_torch.float32, device=dev)
+        tip, tlp = top_ids.data_ptr(), top_logp.data_ptr()
+    st = L.cl_token_logprobs(logits.data_ptr(), dt, row, T, V, ip, C, logp.data_ptr(), entropy.data_ptr(), top_k, tip, tlp,
+                             _stream(dev))
+    if st:
+        _check(st, "cl_token_logprobs")
     return (logp, entropy, top_ids, top_logp) if top_k else (logp, entropy)

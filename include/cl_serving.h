@@ -136,7 +136,8 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  *                    are ignored.
  *   scale            of the scores, finite
  *   work             device, cl_tree_attention_work_bytes(...) bytes for these arguments, 16-byte aligned (may be
- *                    NULL where that is 0).  Holds anything before and after; one call at a time may use it.
+ *                    NULL where that is 0).  Its first CL_ATTENTION_COUNTER_BYTES are zeroed once before its first
+ *                    use; calls leave them zeroed.  One call at a time may use it.
  * Scores, maxima, sums and outputs are held in fp32.  The probabilities enter the matrix cores as fp16,
  * scaled so that no value down to 2^-29 of the largest is lost; keys and values enter exactly.
  * A page of block_table outside the cache, or a place past its width, gives NaN in the rows that see it.
@@ -144,6 +145,7 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  * Deterministic: the same inputs give bitwise identical o.
  * Errors: CL_EINVAL, CL_EUNSUPPORTED (dim, max_q > 256), CL_ESIZE, CL_ENOMEM (work_bytes too small), CL_EHIP.
  */
+#define CL_ATTENTION_COUNTER_BYTES 262144
 size_t cl_tree_attention_work_bytes(int32_t sequences, int32_t q_heads, int32_t heads, int32_t dim, int32_t max_q,
                                     int32_t max_ctx);
 cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_token, int64_t q_head, int32_t tokens,
@@ -164,14 +166,11 @@ cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_token, int64
  *   ids              device, [rows, given] int32 (given may be 0)
  *   logp, entropy    device, [rows, given] and [rows] fp32
  *   top_ids, top_logp  device, [rows, top_k] int32 and fp32 (NULL if top_k is 0); 0 <= top_k <= min(32, vocab)
- *   work             device, cl_token_logprobs_work_bytes(rows, vocab, top_k) bytes, 16-byte aligned; may be
- *                    NULL where that is 0.  Holds anything before and after.
- * Errors: CL_EINVAL, CL_EUNSUPPORTED (top_k > 32), CL_ESIZE (vocab > 2^24), CL_ENOMEM, CL_EHIP.
+ * Errors: CL_EINVAL, CL_EUNSUPPORTED (top_k > 32), CL_ESIZE (vocab > 2^24), CL_EHIP.
  */
-size_t cl_token_logprobs_work_bytes(int32_t rows, int32_t vocab, int32_t top_k);
 cl_status cl_token_logprobs(const void* x, int32_t dtype, int64_t x_row, int32_t rows, int32_t vocab,
                             const int32_t* ids, int32_t given, float* logp, float* entropy, int32_t top_k,
-                            int32_t* top_ids, float* top_logp, void* work, size_t work_bytes, void* stream);
+                            int32_t* top_ids, float* top_logp, void* stream);
 
 #ifdef __cplusplus
 }

@@ -108,8 +108,8 @@ def test_attention_refusals():
 def test_logprobs_refusals():
     L = cla.lib()
 
-    def call(x=P, dtype=0, rows=2, vocab=100, ids=P, given=1, logp=P, ent=P, k=4, ti=P, tl=P, work=P, size=1 << 40):
-        return L.cl_token_logprobs(x, dtype, vocab, rows, vocab, ids, given, logp, ent, k, ti, tl, work, size, None)
+    def call(x=P, dtype=0, rows=2, vocab=100, ids=P, given=1, logp=P, ent=P, k=4, ti=P, tl=P):
+        return L.cl_token_logprobs(x, dtype, vocab, rows, vocab, ids, given, logp, ent, k, ti, tl, None)
 
     for kw in (dict(x=None), dict(ids=None), dict(logp=None), dict(ent=None), dict(ti=None), dict(tl=None), dict(x=ODD),
                dict(dtype=5), dict(rows=-1), dict(vocab=0), dict(given=-1), dict(k=-1), dict(vocab=3)):
