@@ -7,11 +7,13 @@
 // l e^-d); threads, wavefronts and, for few rows, workgroups with parts of the row
 // are joined by the same rule.  log p(i) = x_i - m - log l; entropy = log l - w / l.
 //
-// Alternatives: a wavefront keeps its best top_k logits as 64-bit keys (order of the
-// value, then of the lower id), sorted across its lanes.  One float compare of a
-// logit against the last of them settles nearly every logit; the few that pass are
-// inserted one by one.  A tile first raises that bar to the top_k-th largest of its
-// lanes' maxima, which bounds the insertions whatever the order of the row.
+// Alternatives: logits become 64-bit keys (order of the value, then of the lower id).
+// A tile first finds the top_k-th largest of its lanes' maxima; a logit below that
+// bar, or below an earlier tile's, is none of the top_k, which one float compare
+// settles.  The few that pass are collected in LDS; a wavefront whose list is full
+// keeps its best top_k, whose last then is an exact bar (rows of equal or mostly masked
+// logits).  At the end the candidates above the highest bar of the workgroup are ranked by
+// counting the larger ones: keys are unique, so a rank is a place in the output.
 //
 // Bound by the read of the logits where there are rows for the whole card; a single
 // row by one CU's share of it and the latency of the joins.
@@ -48,11 +50,6 @@ __device__ __forceinline__ float key_value(u64 key) {
   const uint32_t u = (uint32_t)(key >> 32);
   return __builtin_bit_cast(float, (u >> 31) ? u & 0x7FFFFFFFu : ~u);
 }
-__device__ __forceinline__ u64 lane_u64(u64 v, int lane) {
-  return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
-}
-
 // Running maximum and sums of some logits.
 struct Stat {
   float m, l, w;
@@ -71,35 +68,67 @@ __device__ __forceinline__ void join_lanes(Stat& a) {
   for (int d = 1; d < 64; d <<= 1) join(a, Stat{__shfl_xor(a.m, d), __shfl_xor(a.l, d), __shfl_xor(a.w, d)});
 }
 
-// A wavefront's best keys, one to a lane, largest in lane 0; lanes from `k` on are not used.
+constexpr int kList = 128;  // candidates of a wavefront
+
+// Keys of `list` larger than `key`.
+__device__ __forceinline__ int rank_in(const u64* list, int n, u64 key) {
+  int r = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) r += list[i] > key;
+  return r;
+}
+
+// A wavefront's candidates (uniform but for the list in LDS).
 struct Best {
-  u64 key;    // this lane's
-  u64 last;   // the k-th: what a candidate has to beat
-  float bar;  // its value; -inf until k logits have been seen
-  int k;
-  __device__ __forceinline__ void clear(int top_k) {
-    key = last = 0;
-    bar = -INFINITY;
+  u64* list;
+  int k, n;
+  float bar;  // what a logit must not be below
+  u64 last;   // what a key has to beat; 0 until the list was full
+  __device__ __forceinline__ void clear(u64* l, int top_k) {
+    list = l;
     k = top_k;
+    n = 0;
+    bar = -INFINITY;
+    last = 0;
   }
-  // Inserts the keys of the lanes in `who` that beat the last one.
-  __device__ __forceinline__ void insert(u64 cand, u64 who) {
+  // Keeps the best k.
+  __device__ __forceinline__ void shrink() {
     const int lane = threadIdx.x % 64;
-    who &= __ballot(cand > last);
-    while (who) {
-      const int from = __builtin_ctzll(who);
-      const u64 c = lane_u64(cand, from);
-      const int at = __builtin_popcountll(__ballot(key > c));
-      const int hi = __builtin_amdgcn_update_dpp(0, (int)(key >> 32), 0x138, 0xF, 0xF, false);  // from the lane below
-      const int lo = __builtin_amdgcn_update_dpp(0, (int)key, 0x138, 0xF, 0xF, false);
-      if (lane >= at) key = lane == at ? c : (u64)(uint32_t)hi << 32 | (uint32_t)lo;
-      last = lane_u64(key, k - 1);
-      who &= who - 1;
-      who &= __ballot(cand > last);
+    lds_ordered();
+    u64 key[kList / 64];
+    int at[kList / 64];
+#pragma unroll
+    for (int i = 0; i < kList / 64; ++i) {
+      key[i] = lane + 64 * i < n ? list[lane + 64 * i] : 0;
+      at[i] = rank_in(list, n, key[i]);
     }
-    bar = last ? key_value(last) : -INFINITY;
-    if (bar != bar) bar = INFINITY;  // a NaN is the last: only another NaN may pass
+    lds_ordered();
+#pragma unroll
+    for (int i = 0; i < kList / 64; ++i)
+      if (key[i] && at[i] < k) list[at[i]] = key[i];
+    lds_ordered();
+    n = min(n, k);
+    if (n == k) {
+      last = list[k - 1];
+      last = (u64)(uint32_t)__builtin_amdgcn_readfirstlane((int)(last >> 32)) << 32 |
+             (uint32_t)__builtin_amdgcn_readfirstlane((int)last);
+      const float v = key_value(last);
+      bar = fmaxf(bar, v != v ? INFINITY : v);  // a NaN is the last: only another NaN may pass
+    }
   }
+  // Adds the keys of the lanes in `who`.
+  __device__ __forceinline__ void add(u64 key, u64 who) {
+    if (last) who &= __ballot(key > last);
+    if (n + __builtin_popcountll(who) > kList) {
+      shrink();
+      who &= __ballot(key > last);
+    }
+    const int lane = threadIdx.x % 64;
+    if ((who >> lane) & 1) list[n + __builtin_popcountll(who & ((1ull << lane) - 1))] = key;
+    n += __builtin_popcountll(who);
+  }
+  // The order of LDS accesses within the wavefront is theirs in the program.
+  static __device__ __forceinline__ void lds_ordered() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 };
 
 // A row's logits [0, j1), by a workgroup of kThreads.
@@ -153,80 +182,98 @@ __device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ 
     st.w += w;
     // alternatives
     if (best.k) {
-      float bar = best.bar;
-      if (__builtin_popcountll(__ballot(top > bar)) > best.k) {
-        // the k-th largest of the lanes' maxima, found from its highest bit down
+      if (__builtin_popcountll(__ballot(top > best.bar)) > best.k) {
+        // the k-th largest of the lanes' maxima, found from its highest bit down (and rounded down: 20 bits are enough)
         uint32_t u = __builtin_bit_cast(uint32_t, top + 0.0f), at_least = 0;
         u = top != top ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
-        for (int bit = 31; bit >= 0; --bit) {
+        for (int bit = 31; bit >= 12; --bit) {
           const uint32_t to = at_least | 1u << bit;
           if (__builtin_popcountll(__ballot(u >= to)) >= best.k) at_least = to;
         }
-        bar = fmaxf(bar, key_value((u64)at_least << 32));
+        best.bar = fmaxf(best.bar, key_value((u64)at_least << 32));
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const u64 who = __ballot(!(v[i] < bar));  // a NaN passes
+        const u64 who = __ballot(!(v[i] < best.bar));  // a NaN passes
         if (who) {
           const int j = t0 + (i / V * kThreads + tid) * V + i % V;
-          best.insert(rank_key(v[i], j), who & __ballot(j < j1));
-          bar = fmaxf(bar, best.bar);
+          best.add(rank_key(v[i], j), who & __ballot(j < j1));
         }
       }
     }
   }
 }
 
-// Joins the workgroup's wavefronts; the result is in wavefront 0 (st in all its lanes).
-template <int kLpWaves>
-__device__ __forceinline__ void join_waves(Stat& st, Best& best) {
-  __shared__ float s_st[kLpWaves][3];
-  __shared__ u64 s_top[kLpWaves][32];
+// Joins the wavefronts' sums.  A join is not the same to the last bit from both its sides, so every lane takes
+// lane 0's result.
+template <int kWaves>
+__device__ __forceinline__ void join_waves(Stat& st) {
+  __shared__ float s_st[kWaves][3];
   const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
   join_lanes(st);
   if (lane == 0) s_st[wave][0] = st.m, s_st[wave][1] = st.l, s_st[wave][2] = st.w;
-  if (lane < best.k) s_top[wave][lane] = best.key;
   __syncthreads();
-  if (wave) return;
-  // the wavefronts' sums one to a lane, then their keys 64 at a time
-  st = lane < kLpWaves ? Stat{s_st[lane][0], s_st[lane][1], s_st[lane][2]} : Stat{-INFINITY, 0.f, 0.f};
+  st = lane < kWaves ? Stat{s_st[lane][0], s_st[lane][1], s_st[lane][2]} : Stat{-INFINITY, 0.f, 0.f};
   join_lanes(st);
-  const int keys = (kLpWaves - 1) * best.k;
-  for (int k0 = 0; k0 < keys; k0 += 64) {
-    const int i = k0 + lane;
-    best.insert(i < keys ? s_top[1 + i / best.k][i % best.k] : 0, ~0ull);
-  }
-}
-
-// A row's outputs, by wavefront 0.
-template <int DT>
-__device__ __forceinline__ void finish(const LogprobArgs& a, int t, const typename Elem<DT>::raw* x, const Stat& st,
-                                       const Best& best) {
-  const int lane = threadIdx.x % 64;
-  const float lse = __builtin_amdgcn_logf(st.l) * kLn2;
-  if (lane == 0) a.entropy[t] = lse - st.w / st.l;
-  for (int c = lane; c < a.given; c += 64) {
-    const int id = a.ids[(int64_t)t * a.given + c];
-    a.logp[(int64_t)t * a.given + c] = id >= 0 && id < a.vocab ? Elem<DT>::up(x[id]) - st.m - lse : __builtin_nanf("");
-  }
-  if (lane < a.top_k) {
-    const int id = (int)~(uint32_t)best.key;
-    a.top_ids[(int64_t)t * a.top_k + lane] = id;
-    a.top_logp[(int64_t)t * a.top_k + lane] = key_value(best.key) - st.m - lse;
-  }
+  const auto lane0 = [](float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+  };
+  st = Stat{lane0(st.m), lane0(st.l), lane0(st.w)};
 }
 
 // One workgroup a row.
 template <int DT, bool VEC, int kThreads>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
-  const int t = blockIdx.x;
+  constexpr int kWaves = kThreads / 64;
+  __shared__ u64 s_list[kWaves * kList], s_all[kWaves * kList];
+  __shared__ float s_bar[kWaves];
+  __shared__ int s_n;
+  const int t = blockIdx.x, tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const auto* x = static_cast<const typename Elem<DT>::raw*>(a.x) + t * a.x_row;
+  // the first given tokens' logits are asked for at once
+  float mine = __builtin_nanf("");
+  if (tid < a.given) {
+    const int id = a.ids[(int64_t)t * a.given + tid];
+    if (id >= 0 && id < a.vocab) mine = Elem<DT>::up(x[id]);
+  }
+  if (tid == 0) s_n = 0;
   Stat st;
   Best best;
-  best.clear(a.top_k);
+  best.clear(s_list + wave * kList, a.top_k);
   scan<DT, VEC, kThreads>(x, a.vocab, st, best);
-  join_waves<kThreads / 64>(st, best);
-  if (threadIdx.x < 64) finish<DT>(a, t, x, st, best);
+  if (lane == 0) s_bar[wave] = best.bar;
+  join_waves<kWaves>(st);  // a barrier: bars and the cleared count are there
+  const float lse = __builtin_amdgcn_logf(st.l) * kLn2;
+  if (tid == 0) a.entropy[t] = lse - st.w / st.l;
+  for (int c = tid; c < a.given; c += kThreads) {
+    if (c >= kThreads) {
+      const int id = a.ids[(int64_t)t * a.given + c];
+      mine = id >= 0 && id < a.vocab ? Elem<DT>::up(x[id]) : __builtin_nanf("");
+    }
+    a.logp[(int64_t)t * a.given + c] = mine - st.m - lse;
+  }
+  if (!a.top_k) return;
+  // candidates above every wavefront's bar
+  float bar = s_bar[0];
+#pragma unroll
+  for (int v = 1; v < kWaves; ++v) bar = fmaxf(bar, s_bar[v]);
+  for (int i = lane; i < best.n; i += 64) {
+    const u64 key = best.list[i];
+    if (!(key_value(key) < bar)) s_all[atomicAdd(&s_n, 1)] = key;
+  }
+  __syncthreads();
+  const int n = s_n;
+  for (int i = tid / 16; i < n; i += kThreads / 16) {  // 16 lanes a candidate
+    const u64 key = s_all[i];
+    int at = 0;
+    for (int j = tid % 16; j < n; j += 16) at += s_all[j] > key;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) at += __shfl_xor(at, d);
+    if (tid % 16 == 0 && at < a.top_k) {
+      a.top_ids[(int64_t)t * a.top_k + at] = (int)~(uint32_t)key;
+      a.top_logp[(int64_t)t * a.top_k + at] = key_value(key) - st.m - lse;
+    }
+  }
 }
 
 template <int DT, int kThreads>
@@ -239,8 +286,9 @@ void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
 
 template <int DT>
 void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
-  // four wavefronts a row where the rows fill the card, sixteen where they do not
-  if (rows >= 512)
+  // Sixteen wavefronts a row while the rows leave CUs free (256 x 32000: 13.2 against 18.1 us; 384: 21.4 against
+  // 19.4); four for more rows, or where they hold a row in one tile (256 x 5000: 7.3 against 10.0).
+  if (rows > 256 || a.vocab <= 256 * kPer)
     launch_logprobs<DT, 256>(a, rows, vec, s);
   else
     launch_logprobs<DT, 1024>(a, rows, vec, s);

@@ -314,14 +314,18 @@ def token_logprobs(logits, ids, top_k: int = 0):
         raise ValueError(f"ids must be int32 [{T}, given]")
     C = ids.shape[1]
     ip = _index(ids, T * C, dev, "ids")
-    logp = _empty((T, C), dtype=_torch.float32, device=dev)
-    entropy = _empty((T,), dtype=_torch.float32, device=dev)
+    # the outputs are pieces of one allocation
+    n = T * C
+    buf = _empty(n + T + 2 * T * max(top_k, 0), dtype=_torch.float32, device=dev)
+    at = buf.data_ptr()
+    logp, entropy = buf.as_strided((T, C), (C, 1), 0), buf.as_strided((T,), (1,), n)
     top_ids = top_logp = tip = tlp = None
     if top_k > 0:
-        top_ids = _empty((T, top_k), dtype=_i32, device=dev)
-        top_logp = _empty((T, top_k), dtype=_torch.float32, device=dev)
-        tip, tlp = top_ids.data_ptr(), top_logp.data_ptr()
-    st = L.cl_token_logprobs(logits.data_ptr(), dt, row, T, V, ip, C, logp.data_ptr(), entropy.data_ptr(), top_k, tip, tlp,
+        top_logp = buf.as_strided((T, top_k), (top_k, 1), n + T)
+        top_ids = buf.view(_i32).as_strided((T, top_k), (top_k, 1), n + T + T * top_k)
+        tlp = at + 4 * (n + T)
+        tip = tlp + 4 * T * top_k
+    st = L.cl_token_logprobs(logits.data_ptr(), dt, row, T, V, ip, C, at, at + 4 * n, top_k, tip, tlp,
                              _stream(dev))
     if st:
         _check(st, "cl_token_logprobs")
