@@ -43,11 +43,12 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBlock = 32;         // keys of a wavefront's step
 constexpr int kWaves = 4;
+constexpr int kWideRows = 128;     // query rows of a workgroup of the wide kernel
 constexpr float kNone = -3.4e38f;  // running maximum before any key
 constexpr float kSlack = 4.f;      // log2 by which a score may pass the running maximum
 constexpr int kProbBits = 11;      // probabilities are scaled by 2^11: with the slack at most 2^15
 
-constexpr int kMaxChunk = 2048;    // keys of a workgroup
+constexpr int kMaxChunk = 4096;    // keys of a workgroup
 constexpr int kInline = 8;         // chunks that the last workgroup of a cell joins; more are joined by a launch
 constexpr int kMaxCells = 65536;   // cells (sequence, kv head, row group) that may be joined so: their counters open the workspace
 constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
@@ -105,6 +106,12 @@ __device__ __forceinline__ Range range_of(const AttnArgs& a, int first, int end,
   return x;
 }
 
+// Largest of three, NaN if one is.  (fmaxf would first quiet each operand whose origin the compiler cannot see, an
+// instruction apiece.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
 // Largest value of the four lanes that hold parts of one row (16 apart).
 __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
@@ -122,10 +129,19 @@ __device__ __forceinline__ uint32_t widen8(uint32_t pair) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
-// Nibbles `at` (0, 4, 8 or 12) of the two halves of a word -> (nibble - 8) * s, exactly (s of 8 significant bits).
-__device__ __forceinline__ uint32_t widen4(uint32_t word, int at, h2 s) {
-  const uint32_t n = ((word >> at) & 0x000F000Fu) | 0x64006400u;  // 1024 + nibble
-  const h2 c = __builtin_bit_cast(h2, n) - h2{(_Float16)1032.f, (_Float16)1032.f};
+// Nibbles `i` of the two halves of a word -> (nibble - 8) * s, exactly (s of 8 significant bits).  word8 is word >> 8: a nibble
+// in the second place becomes 1024 + 16 nibble, which a fused multiply-add takes down as exactly as an addition
+// 1024 + nibble.
+__device__ __forceinline__ uint32_t widen4(uint32_t word, uint32_t word8, int i, h2 s) {
+  const uint32_t w = i & 2 ? word8 : word;
+  uint32_t exponent = 0x64006400u;
+  asm("" : "+v"(exponent));  // in a register, so that mask and exponent are one instruction
+  h2 c;
+  if (i & 1)
+    c = __builtin_elementwise_fma(__builtin_bit_cast(h2, (w & 0x00F000F0u) | exponent),
+                                  h2{(_Float16)0.0625f, (_Float16)0.0625f}, h2{(_Float16)-72.f, (_Float16)-72.f});
+  else
+    c = __builtin_bit_cast(h2, (w & 0x000F000Fu) | exponent) - h2{(_Float16)1032.f, (_Float16)1032.f};
   return __builtin_bit_cast(uint32_t, c * s);
 }
 
@@ -138,14 +154,183 @@ struct Scales<CL_KV_INT8> {
 };
 template <>
 struct Scales<CL_KV_INT4> {
-  uint16_t k[2];  // of key l % 16, the lane's channels
-  uint16_t v[8];  // of keys 4 (l / 16) .. of either tile, the lane's channels
+  uint32_t k[2];  // of key l % 16, the lane's channels
+  uint32_t v[8];  // of keys 4 (l / 16) .. of either tile, the lane's channels
 };
 
-// Channel of step s, slot j (0..7) of lane group g in the first product.
-template <int KIND, int D>
-__device__ __forceinline__ constexpr int q_channel(int s, int g) {
-  return KIND == CL_KV_INT8 ? (s / 2) * 64 + 16 * g + (s % 2) * 8 : (D / 4) * g + 8 * s;
+// What a lane keeps of RT query rows: row l % 16 of each tile.
+template <int RT>
+struct Rows {
+  float rowc[RT];         // what turns a product of operands into a score, in log2
+  float top[RT];          // running maximum of the scores
+  float m[RT];            // it less log2(2^kProbBits / vref): sum and the outputs carry that factor, which the quotient loses
+  float sum[RT];
+  int tok[RT];            // its new token
+  float vref;             // a power of two above every V scale seen (int4, where V carries its scales: 1)
+};
+
+// The first RT x 16 rows from `row0` of Q, raw.
+template <int RT, int STEPS, typename Channel>
+__device__ __forceinline__ void load_q(const AttnArgs& a, int first, int n_new, int hk, int row0, Channel channel, Rows<RT>& rows,
+                                       u4 (&raw)[RT][STEPS]) {
+  const int c16 = threadIdx.x & 15, G = a.group;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = row0 + 16 * r + c16;
+    rows.tok[r] = row / G;
+    const bool there = rows.tok[r] < n_new;  // otherwise the values are not used
+    const uint16_t* qp = a.q + (int64_t)(first + (there ? rows.tok[r] : 0)) * a.q_token + (int64_t)(hk * G + row % G) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) raw[r][s] = *reinterpret_cast<const u4*>(qp + channel(s));
+  }
+}
+
+// Q as the second operand: scaled by a power of two into fp16's range.  An int4 piece of 8 channels is taken in the order
+// 0, 4, 1, 5, 2, 6, 3, 7, as its nibbles come.
+template <int KIND, int RT, int STEPS>
+__device__ __forceinline__ void convert_q(const AttnArgs& a, const u4 (&raw)[RT][STEPS], Rows<RT>& rows, uint32_t (&q)[RT][STEPS][4]) {
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float f[STEPS][8], top = 0.f;
+    bool fine = true;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint16_t e = (uint16_t)(raw[r][s][j / 2] >> (16 * (j % 2)));
+        f[s][j] = a.bf16 ? Elem<CL_BF16>::up(e) : Elem<CL_F16>::up(e);
+        fine = fine && fabsf(f[s][j]) < INFINITY;
+        top = fmaxf(top, fabsf(f[s][j]));
+      }
+    }
+    top = row_max(top);
+    fine = row_max(fine ? 0.f : 1.f) == 0.f;
+    int e = 0;
+    (void)frexpf(top, &e);
+    if (!(top > 0.f) || !fine) e = 0;
+    // a row with an infinity or NaN is NaN; a negative scale turns Q around, so that rowc >= 0
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int lo = KIND == CL_KV_INT8 ? 2 * j : j, hi = KIND == CL_KV_INT8 ? 2 * j + 1 : j + 4;
+        float x = ldexpf(f[s][lo], 14 - e), y = ldexpf(f[s][hi], 14 - e);
+        if (a.scale < 0.f) x = -x, y = -y;
+        if (a.scale == 0.f) x = y = 0.f;
+        if (!fine) x = y = __builtin_nanf("");
+        q[r][s][j] = __builtin_bit_cast(uint32_t, h2{(_Float16)x, (_Float16)y});
+      }
+    // above zero, so that a masked score of -inf stays what it is
+    rows.rowc[r] = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e - 14 + (KIND == CL_KV_INT8 ? 9 : 0)), 1e-38f);
+    rows.top[r] = rows.m[r] = kNone;
+    rows.sum[r] = 0.f;
+  }
+  rows.vref = KIND == CL_KV_INT8 ? 0.f : 1.f;
+}
+
+// Scores of a block of 32 keys from its products: K's scales (int8), and for a block that some rows do not see whole the
+// masks.  s[r][t][i]: row l % 16 of tile r, key 16 t + 4 (l / 16) + i; j0: the block's first key; left: keys of it that exist;
+// bad: tiles without a page.  ks, vs: the scales of those keys (int8).
+template <int KIND, int RT>
+__device__ __forceinline__ void finish_scores(const AttnArgs& a, const Range& range, const Rows<RT>& rows, const float (&ks)[8],
+                                              uint32_t j0, int left, int bad, bool special, f4 (&s)[RT][2], float (&vs)[8]) {
+  const int g = (threadIdx.x & 63) >> 4;
+  if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s[r][j / 4][j % 4] *= ks[j];
+  }
+  if (!special) return;
+  if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (16 * (j / 4) + 4 * g + j % 4 >= left) vs[j] = 0.f;  // no token there: the scale may be anything
+  }
+  const int64_t rel = (int64_t)j0 - range.ctx;  // place of the block's first key among the new tokens
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    uint32_t see;  // keys of the block that the row sees
+    if (!a.mask) {
+      const int64_t cnt = rows.tok[r] - rel + 1;
+      see = cnt >= 32 ? ~0u : cnt <= 0 ? 0u : (1u << cnt) - 1u;
+    } else if (rel <= -32) {
+      see = ~0u;
+    } else {
+      const uint64_t* w = a.mask + (int64_t)(range.first + min(rows.tok[r], range.n_new - 1)) * a.mask_words;
+      if (rel < 0) {
+        see = (uint32_t)(w[0] << -rel) | ((1u << -rel) - 1u);
+      } else {
+        const int at = (int)(rel >> 6), sh = (int)(rel & 63);
+        uint64_t bits = at < a.mask_words ? w[at] >> sh : 0;
+        if (sh > 32 && at + 1 < a.mask_words) bits |= w[at + 1] << (64 - sh);
+        see = (uint32_t)bits;
+      }
+    }
+    if (left < 32) see &= (1u << left) - 1u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int key = 16 * (j / 4) + 4 * g + j % 4;
+      if (!((see >> key) & 1))
+        s[r][j / 4][j % 4] = -INFINITY;
+      else if ((bad >> (j / 4)) & 1)
+        s[r][j / 4][j % 4] = __builtin_nanf("");
+    }
+  }
+}
+
+// Probabilities of a block from its scores, as the operand of the second product; moves the running maximum, and with it
+// sums and outputs, where a score passes it by more than the slack.
+template <int KIND, int RT, int CB>
+__device__ __forceinline__ void probabilities(const f4 (&s)[RT][2], const float (&vs)[8], Rows<RT>& rows, f4 (&o)[RT][CB],
+                                              uint32_t (&p)[RT][4]) {
+  float up[RT];
+  bool move = false;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float t = max3(max3(s[r][0][0], s[r][0][1], s[r][0][2]), max3(s[r][0][3], s[r][1][0], s[r][1][1]),
+                         max3(s[r][1][2], s[r][1][3], s[r][1][3]));
+    up[r] = t * rows.rowc[r];
+    move |= up[r] > rows.top[r] + kSlack;
+  }
+  float vtop = 0.f;
+  if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) vtop = max3(vtop, vs[j], vs[j + 1]);
+    move |= vtop > rows.vref;
+  }
+  if (__any(move)) {
+    float to = rows.vref;
+    if constexpr (KIND == CL_KV_INT8) {
+      vtop = row_max(vtop);
+      if (vtop > to) to = 2.f * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, vtop) & 0x7F800000u);
+    }
+    const float lift = to > 0.f ? __builtin_amdgcn_logf(to) - kProbBits : 0.f;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      // only a row that passed it, so that no row's roundings depend on another's
+      const float high = row_max(up[r]);
+      if (high > rows.top[r] + kSlack) rows.top[r] = high;
+      const float next = rows.top[r] + lift, old = __builtin_amdgcn_exp2f(rows.m[r] - next);
+      rows.m[r] = next;
+      rows.sum[r] *= old;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) o[r][cb] *= old;
+    }
+    rows.vref = to;
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    float e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      e[j] = __builtin_amdgcn_exp2f(s[r][j / 4][j % 4] * rows.rowc[r] - rows.m[r]);
+      rows.sum[r] += e[j];
+      if constexpr (KIND == CL_KV_INT8) e[j] *= vs[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[r][j] = __builtin_bit_cast(uint32_t, h2{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
+  }
 }
 
 // 16 bytes of each lane straight into LDS, lane l's at `to` + 16 l; not kept in the caches (aux 2), which is worth a tenth of
@@ -302,65 +487,17 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   Scales<KIND> sc_next;
   int bad_next = 0;
   if (steps > 0) bad_next = load(0, sc_next);
+  Rows<RT> st;
   u4 raw[RT][STEPS];
-  int tok[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int row = rg * ROWS + 16 * r + c16;
-    tok[r] = row / G;
-    const bool there = tok[r] < n_new;  // otherwise the values are not used
-    const uint16_t* qp = a.q + (int64_t)(first + (there ? tok[r] : 0)) * a.q_token + (int64_t)(hk * G + row % G) * a.q_head;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) raw[r][s] = *reinterpret_cast<const u4*>(qp + q_channel<KIND, D>(s, g));
-  }
-  // ---- Q: rows n = l % 16 of each tile, scaled by a power of two, as the second operand
+  load_q(a, first, n_new, hk, rg * ROWS,
+         [&](int s) { return KIND == CL_KV_INT8 ? (s / 2) * 64 + 16 * g + (s % 2) * 8 : (D / 4) * g + 8 * s; }, st, raw);
   uint32_t q[RT][STEPS][4];
-  float rowc[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float f[STEPS][8], top = 0.f;
-    bool fine = true;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint16_t e = (uint16_t)(raw[r][s][j / 2] >> (16 * (j % 2)));
-        f[s][j] = a.bf16 ? Elem<CL_BF16>::up(e) : Elem<CL_F16>::up(e);
-        fine = fine && fabsf(f[s][j]) < INFINITY;
-        top = fmaxf(top, fabsf(f[s][j]));
-      }
-    }
-    top = row_max(top);
-    fine = row_max(fine ? 0.f : 1.f) == 0.f;
-    int e = 0;
-    (void)frexpf(top, &e);
-    if (!(top > 0.f) || !fine) e = 0;
-    // a row with an infinity or NaN is NaN; a negative scale turns Q around, so that rowc >= 0
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int lo = KIND == CL_KV_INT8 ? 2 * j : j, hi = KIND == CL_KV_INT8 ? 2 * j + 1 : j + 4;
-        float x = ldexpf(f[s][lo], 14 - e), y = ldexpf(f[s][hi], 14 - e);
-        if (a.scale < 0.f) x = -x, y = -y;
-        if (a.scale == 0.f) x = y = 0.f;
-        if (!fine) x = y = __builtin_nanf("");
-        q[r][s][j] = __builtin_bit_cast(uint32_t, h2{(_Float16)x, (_Float16)y});
-      }
-    // above zero, so that a masked score of -inf stays what it is
-    rowc[r] = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e - 14 + (KIND == CL_KV_INT8 ? 9 : 0)), 1e-38f);
-  }
-
+  convert_q<KIND>(a, raw, st, q);
   f4 o[RT][CB];
-  float top[RT], m[RT], sum[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    top[r] = m[r] = kNone;
-    sum[r] = 0.f;
+  for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) o[r][cb] = f4{0.f, 0.f, 0.f, 0.f};
-  }
-  float vref = KIND == CL_KV_INT8 ? 0.f : 1.f;  // a power of two above every V scale seen (int4: V carries its scales)
 
   for (int i = 0; i < steps; ++i) {
     // the block moves from LDS into registers, then the next one flies for a whole step
@@ -411,114 +548,26 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
           for (int j = 0; j < 4; ++j)
             k[j] = widen8(perm(0, raw[2 * (st % 2) + j / 2], j % 2 ? 0x0C030C02u : 0x0C010C00u));
         } else {
-          const h2 ks = __builtin_bit_cast(h2, (uint32_t)sc.k[t] * 0x10001u);
+          const h2 ks = __builtin_bit_cast(h2, sc.k[t] | sc.k[t] << 16);
+          const uint32_t w = kr[t][0][st], w8 = w >> 8;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) k[j] = widen4(kr[t][0][st], 4 * j, ks);
+          for (int j = 0; j < 4; ++j) k[j] = widen4(w, w8, j, ks);
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r][t] = mfma16(k, q[r][st], s[r][t]);
       }
     }
-    if constexpr (KIND == CL_KV_INT8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float ks = Elem<CL_F16>::up((uint16_t)(sc.k[j / 4][j % 4 / 2] >> (16 * (j % 2))));
-#pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][j / 4][j % 4] *= ks;
-      }
-    }
-    float vs[8];
-    if constexpr (KIND == CL_KV_INT8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vs[j] = Elem<CL_F16>::up((uint16_t)(sc.v[j / 4][j % 4 / 2] >> (16 * (j % 2))));
-    }
-    if (special) {
-      if constexpr (KIND == CL_KV_INT8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (16 * (j / 4) + 4 * g + j % 4 >= left) vs[j] = 0.f;  // no token there: the scale may be anything
-      }
-      const int64_t rel = (int64_t)j0 - ctx;  // place of the block's first key among the new tokens
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        uint32_t see;  // keys of the block that the row sees
-        if (!a.mask) {
-          const int64_t cnt = tok[r] - rel + 1;
-          see = cnt >= 32 ? ~0u : cnt <= 0 ? 0u : (1u << cnt) - 1u;
-        } else if (rel <= -32) {
-          see = ~0u;
-        } else {
-          const uint64_t* w = a.mask + (int64_t)(first + min(tok[r], n_new - 1)) * a.mask_words;
-          if (rel < 0) {
-            see = (uint32_t)(w[0] << -rel) | ((1u << -rel) - 1u);
-          } else {
-            const int at = (int)(rel >> 6), sh = (int)(rel & 63);
-            uint64_t bits = at < a.mask_words ? w[at] >> sh : 0;
-            if (sh > 32 && at + 1 < a.mask_words) bits |= w[at + 1] << (64 - sh);
-            see = (uint32_t)bits;
-          }
-        }
-        if (left < 32) see &= (1u << left) - 1u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int key = 16 * (j / 4) + 4 * g + j % 4;
-          if (!((see >> key) & 1))
-            s[r][j / 4][j % 4] = -INFINITY;
-          else if ((bad >> (j / 4)) & 1)
-            s[r][j / 4][j % 4] = __builtin_nanf("");
-        }
-      }
-    }
-    // ---- the running maximum, and the largest V scale
-    float up[RT];
-    bool move = false;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float t = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                      fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      up[r] = t * rowc[r];
-      move |= up[r] > top[r] + kSlack;
-    }
-    float vtop = 0.f;
-    if constexpr (KIND == CL_KV_INT8) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vtop = fmaxf(vtop, vs[j]);
-      move |= vtop > vref;
-    }
-    if (__any(move)) {
-      float to = vref;
-      if constexpr (KIND == CL_KV_INT8) {
-        vtop = row_max(vtop);
-        if (vtop > vref) to = 2.f * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, vtop) & 0x7F800000u);
-      }
-      // m is the running maximum less log2(2^kProbBits / vref): sum and o carry that factor, which the quotient loses
-      const float lift = to > 0.f ? __builtin_amdgcn_logf(to) - kProbBits : 0.f;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        top[r] = fmaxf(top[r], row_max(up[r]));
-        const float next = top[r] + lift, old = __builtin_amdgcn_exp2f(m[r] - next);
-        m[r] = next;
-        sum[r] *= old;
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb) o[r][cb] *= old;
-      }
-      vref = to;
-    }
-    // ---- probabilities
+    float ks[8], vs[8];
     uint32_t p[RT][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float e[8];
+    if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        e[j] = __builtin_amdgcn_exp2f(s[r][j / 4][j % 4] * rowc[r] - m[r]);
-        sum[r] += e[j];
-        if constexpr (KIND == CL_KV_INT8) e[j] *= vs[j];
+        ks[j] = Elem<CL_F16>::up((uint16_t)(sc.k[j / 4][j % 4 / 2] >> (16 * (j % 2))));
+        vs[j] = Elem<CL_F16>::up((uint16_t)(sc.v[j / 4][j % 4 / 2] >> (16 * (j % 2))));
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        p[r][j] = __builtin_bit_cast(uint32_t, h2{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
     }
+    finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs);
+    probabilities<KIND>(s, vs, st, o, p);
     // ---- output
     if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
@@ -532,16 +581,19 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
       }
     } else {
       h2 mul[4];
+      uint32_t vsc[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vsc[j] = sc.v[j];
+      if (special) {  // where there is no token the scale may be anything
+        asm volatile("");  // a branch, not eight selects a block
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (16 * (j / 4) + 4 * g + j % 4 >= left) vsc[j] = 0;
+      }
       uint32_t lo[4], hi[4];  // channels 0..3 and 4..7 of two keys, one in each half
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t s0 = sc.v[2 * j], s1 = sc.v[2 * j + 1];
-        if (special) {  // no token there: the scale may be anything
-          const int key = 16 * (j / 2) + 4 * g + 2 * (j % 2);
-          if (key >= left) s0 = 0;
-          if (key + 1 >= left) s1 = 0;
-        }
-        mul[j] = __builtin_bit_cast(h2, s0 | s1 << 16);
+        mul[j] = __builtin_bit_cast(h2, vsc[2 * j] | vsc[2 * j + 1] << 16);
         lo[j] = perm(vr[2 * j + 1].x, vr[2 * j].x, 0x05040100u);
         hi[j] = perm(vr[2 * j + 1].x, vr[2 * j].x, 0x07060302u);
       }
@@ -549,7 +601,10 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
       for (int cb = 0; cb < CB; ++cb) {
         uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = widen4(cb < 4 ? lo[j] : hi[j], 4 * (cb % 4), mul[j]);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t w = cb < 4 ? lo[j] : hi[j];
+          v[j] = widen4(w, w >> 8, cb % 4, mul[j]);
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) o[r][cb] = mfma16(v, p[r], o[r][cb]);
       }
@@ -561,9 +616,9 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   constexpr float unit = KIND == CL_KV_INT8 ? 512.f : 1.f;  // codes entered as code * 2^-9
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    const float l_row = row_sum(sum[r]);
+    const float l_row = row_sum(st.sum[r]);
     const int row = 16 * r + c16;
-    if (g == 0) s_ml[wave][row] = make_float2(m[r], l_row);
+    if (g == 0) s_ml[wave][row] = make_float2(st.m[r], l_row);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -642,6 +697,233 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   }
 }
 
+// Many query rows of a kv head (trees of a grouped model): a workgroup has 128 rows, 32 to a wavefront, and all of them read the
+// same keys.  Its threads widen a block of 32 keys together, K as rows of fp16 and V transposed, into one of two LDS
+// buffers while the products run on the other; so a code is widened once for 128 rows, and an operand is one 16-byte read.
+// Bound by the vector instructions of the softmax beside the products.
+template <int KIND, int D>
+__global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a) {
+  constexpr int RT = 2, STEPS = D / 32, CB = D / 16, ROWS = kWideRows;
+  constexpr int ROWB = KIND == CL_KV_INT8 ? D : D / 2, SC = KIND == CL_KV_INT8 ? 1 : D / 32;
+  constexpr int KB = 32 * D * 2;        // bytes of a block's K as fp16
+  constexpr int VS = 80;                // bytes between the channels of a block's V: 32 keys and padding
+  constexpr int KT = ROWB / 8;          // bytes of K that a thread widens: an eighth of a row
+  constexpr int VC = D / 32;            // channels of V that a thread widens, of four keys
+  __shared__ __align__(1024) uint8_t s_mem[2][KB + D * VS];
+  __shared__ __align__(16) float s_scale[2][2][32];  // int8: K's and V's scales of a block
+  __shared__ int s_bad[2];                           // its tiles without a page
+
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, c16 = l & 15, g = l >> 4;
+  const int b = blockIdx.y, hk = blockIdx.x % a.c.heads, rg = blockIdx.x / a.c.heads, split = blockIdx.z;
+  const Range range = range_of(a, a.cu_q[b], a.cu_q[b + 1], a.ctx_lens[b], gridDim.z);
+  const int first = range.first, n_new = range.n_new;
+  const int G = a.group, rows_left = n_new * G - rg * ROWS;
+  if (rows_left <= 0 || split >= range.splits) return;
+  const uint32_t n = range.n, k0 = split * range.chunk;
+  const int blocks = (int)((min(n - k0, range.chunk) + kBlock - 1) / kBlock);
+  const bool active = wave * 32 < rows_left;  // whether the wavefront has rows
+
+  // pages of the next 64 tiles of 16 keys, one to a lane: -1 outside the cache or the table, 0 past the end
+  int pages = 0;
+  const auto load_pages = [&](int i) {
+    const uint32_t at = k0 + (uint32_t)(i + (l >> 1)) * kBlock + 16 * (l & 1), col = at >> a.page_shift;
+    int p = 0;
+    if (i + (l >> 1) < blocks && at < n) {
+      p = col < (uint32_t)a.table_width ? a.block_table[(int64_t)b * a.table_width + col] : -1;
+      if (p < 0 || p >= a.c.pages) p = -1;
+    }
+    pages = p;
+  };
+  const int in_page = (1 << (a.page_shift - 4)) - 1;
+  const auto row_of = [&](int i, int t, int* bad) -> int64_t {
+    int page = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + t);
+    if (page < 0) *bad |= 1 << t, page = 0;
+    const int tile = (int)((k0 + (uint32_t)i * kBlock) >> 4) + t;
+    return (((int64_t)page * a.c.heads + hk) << a.page_shift) + ((tile & in_page) << 4);
+  };
+
+  // ---- a thread's share of a block: an eighth of K's row tid / 8; VC channels of V's keys 4 (tid / 32) ..  A wavefront's share
+  // lies in one tile
+  const int krow = tid >> 3, kpart = tid & 7, vkey = 4 * (tid >> 5), vch = VC * (tid & 31);
+  struct Raw {
+    u4 k;
+    uint32_t v[4];
+    uint16_t ks, vs[4];  // int4; int8: ks is K's or V's scale of key tid % 32, by the first 64 threads
+    int bad;
+  };
+  const auto load = [&](int i, Raw& x) {
+    if ((i & 31) == 0) load_pages(i);
+    x.bad = 0;
+    int64_t row[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) row[t] = row_of(i, t, &x.bad);
+    const int64_t mine = wave < 2 ? row[0] : row[1];
+    const uint8_t* kp = static_cast<const uint8_t*>(a.c.k) + mine * ROWB + (uint32_t)((krow & 15) * ROWB + kpart * KT);
+    if constexpr (KT == 16) {
+      x.k = *reinterpret_cast<const u4*>(kp);
+    } else if constexpr (KT == 8) {
+      const u2 w = *reinterpret_cast<const u2*>(kp);
+      x.k.x = w.x, x.k.y = w.y;
+    } else {
+      x.k.x = *reinterpret_cast<const uint32_t*>(kp);
+    }
+    const uint8_t* vp = static_cast<const uint8_t*>(a.c.v) + mine * ROWB +
+                        (uint32_t)((vkey & 15) * ROWB + (KIND == CL_KV_INT8 ? vch : vch / 2));
+    constexpr int VB = KIND == CL_KV_INT8 ? VC : VC / 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (VB == 4)
+        x.v[j] = *reinterpret_cast<const uint32_t*>(vp + j * ROWB);
+      else if constexpr (VB == 2)
+        x.v[j] = *reinterpret_cast<const uint16_t*>(vp + j * ROWB);
+      else
+        x.v[j] = vp[j * ROWB];
+    }
+    if constexpr (KIND == CL_KV_INT8) {
+      if (wave == 0) x.ks = (l < 32 ? a.c.k_scale : a.c.v_scale)[((l & 16) ? row[1] : row[0]) + (l & 15)];
+    } else {
+      x.ks = a.c.k_scale[mine * SC + (krow & 15) * SC + kpart * (D / 8) / 32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x.vs[j] = a.c.v_scale[mine * SC + ((vkey & 15) + j) * SC + vch / 32];
+    }
+  };
+  // Widens it into a buffer.  K: row r's 16-byte piece j (8 channels) at place j ^ (r mod pieces); V: channel c's 32 keys in the
+  // order of the second product's slots (slot 8 g + i is key 4 g + i, slot 8 g + 4 + i key 16 + 4 g + i).  The padding
+  // spreads the channels that lanes read together over the banks, and the turn (lanes start at different ones of
+  // their channels) those that they write together.
+  constexpr int PIECES = D / 8;
+  const auto widen = [&](const Raw& x, int i) {
+    uint8_t* const to = s_mem[i & 1];
+    const int left = (int)min(n - (k0 + (uint32_t)i * kBlock), (uint32_t)kBlock);
+    if (tid == 0) s_bad[i & 1] = x.bad;
+    if (KIND == CL_KV_INT8 && wave == 0) (&s_scale[i & 1][0][0])[l] = Elem<CL_F16>::up(x.ks);
+    u4 piece[D / 64];
+#pragma unroll
+    for (int p = 0; p < D / 64; ++p) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (KIND == CL_KV_INT8)
+          piece[p][j] = widen8(perm(0, x.k[2 * p + j / 2], j % 2 ? 0x0C030C02u : 0x0C010C00u));
+        else
+          piece[p][j] = widen4(x.k[p], x.k[p] >> 8, j, __builtin_bit_cast(h2, (uint32_t)x.ks * 0x10001u));
+      }
+      const uint32_t j = kpart * (D / 64) + p;
+      *reinterpret_cast<u4*>(to + krow * (2 * D) + ((j ^ (krow & (PIECES - 1))) << 4)) = piece[p];
+    }
+    uint8_t* const vt = to + KB + (16 * ((vkey & 15) >> 2) + 8 * (vkey >> 4));
+    const int turn = VC == 4 ? (tid & 31) >> 2 : (tid & 31) >> 3;
+    if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        const int own = (c + turn) & (VC - 1);
+        const uint32_t sel = 0x0C040C00u + 0x00010001u * own;
+        *reinterpret_cast<u2*>(vt + (vch + own) * VS) = u2{widen8(perm(x.v[1], x.v[0], sel)), widen8(perm(x.v[3], x.v[2], sel))};
+      }
+    } else {
+      h2 mul[2];
+      uint32_t w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // no token there: the scale may be anything
+        const uint32_t s0 = vkey + 2 * j < left ? x.vs[2 * j] : 0, s1 = vkey + 2 * j + 1 < left ? x.vs[2 * j + 1] : 0;
+        mul[j] = __builtin_bit_cast(h2, s0 | s1 << 16);
+        w[j] = x.v[2 * j] | x.v[2 * j + 1] << 16;
+      }
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        const int own = (c + turn) & (VC - 1);
+        *reinterpret_cast<u2*>(vt + (vch + own) * VS) = u2{widen4(w[0] >> 4 * own, 0, 0, mul[0]), widen4(w[1] >> 4 * own, 0, 0, mul[1])};
+      }
+    }
+  };
+  Raw x;
+  load(0, x);
+  Rows<RT> st;
+  u4 raw[RT][STEPS];
+  load_q(a, first, n_new, hk, rg * ROWS + 32 * wave, [&](int s) { return 32 * s + 8 * g; }, st, raw);
+  uint32_t q[RT][STEPS][4];
+  convert_q<KIND>(a, raw, st, q);
+  f4 o[RT][CB];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) o[r][cb] = f4{0.f, 0.f, 0.f, 0.f};
+  widen(x, 0);
+  if (blocks > 1) load(1, x);
+
+  for (int i = 0; i < blocks; ++i) {
+    __syncthreads();  // block i is widened; the other buffer is free
+    if (i + 1 < blocks) widen(x, i + 1);
+    if (i + 2 < blocks) load(i + 2, x);
+    if (!active) continue;
+    const uint8_t* const kt = s_mem[i & 1];
+    const uint8_t* const vt = kt + KB;
+    const uint32_t j0 = k0 + (uint32_t)i * kBlock;
+    const int left = (int)min(n - j0, (uint32_t)kBlock), bad = __builtin_amdgcn_readfirstlane(s_bad[i & 1]);
+    const bool special = j0 + kBlock > (uint32_t)range.ctx || bad;
+    f4 s[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s[r][0] = s[r][1] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        const u4 w = *reinterpret_cast<const u4*>(kt + (16 * t + c16) * (2 * D) + (((4 * k + g) ^ (c16 & (PIECES - 1))) << 4));
+        const uint32_t kk[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r][t] = mfma16(kk, q[r][k], s[r][t]);
+      }
+    float ks[8], vs[8];
+    if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f4 k4 = *reinterpret_cast<const f4*>(&s_scale[i & 1][0][16 * t + 4 * g]);
+        const f4 v4 = *reinterpret_cast<const f4*>(&s_scale[i & 1][1][16 * t + 4 * g]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ks[4 * t + j] = k4[j], vs[4 * t + j] = v4[j];
+      }
+    }
+    u4 vf[CB];  // V's operands, asked for before the softmax
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) vf[cb] = *reinterpret_cast<const u4*>(vt + (16 * cb + c16) * VS + 16 * g);
+    uint32_t p[RT][4];
+    finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs);
+    probabilities<KIND>(s, vs, st, o, p);
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) {
+      const u4 w = vf[cb];
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int r = 0; r < RT; ++r) o[r][cb] = mfma16(v, p[r], o[r][cb]);
+    }
+  }
+  if (!active) return;
+
+  // ---- each wavefront has its rows whole: lane (row l % 16, channels 16 cb + 4 g ..)
+  constexpr float unit = KIND == CL_KV_INT8 ? 512.f : 1.f;  // codes entered as code * 2^-9
+  const int64_t cell = ((int64_t)b * a.c.heads + hk) * a.row_groups + rg;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int row = 32 * wave + 16 * r + c16;
+    const float den = row_sum(st.sum[r]);
+    if (row >= rows_left) continue;
+    if (range.splits == 1) {
+      const float inv = den == 0.f ? 0.f : unit / den;
+      const int at = rg * ROWS + row;
+      uint16_t* op = a.o + ((int64_t)(first + at / G) * (a.c.heads * G) + hk * G + at % G) * D + 4 * g;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb)
+        *reinterpret_cast<u2*>(op + 16 * cb) = u2{pack16(a.bf16, o[r][cb][0] * inv, o[r][cb][1] * inv),
+                                                 pack16(a.bf16, o[r][cb][2] * inv, o[r][cb][3] * inv)};
+    } else {
+      const int64_t at = (cell * gridDim.z + split) * ROWS + row;
+      if (g == 0) a.part_ml[at] = make_float2(st.m[r], den);
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) *reinterpret_cast<f4*>(a.part_o + at * D + 16 * cb + 4 * g) = o[r][cb] * unit;
+    }
+  }
+}
+
 // Joins the partial outputs of a row's chunks, in chunk order within each of eight strands and the strands in
 // order: 32 lanes (dim 128) or 16 hold four channels each.  For more than kInline chunks this launch of its own, where
 // as many workgroups as there are rows read the partials, beats one workgroup that reads them all.
@@ -699,7 +981,8 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, in
 
 // How a launch is cut: rows to a workgroup, row groups, chunks of keys.
 struct AttnPlan {
-  int rt, row_groups, splits, chunk;
+  bool wide;
+  int group_rows, row_groups, splits, chunk;  // rows of a row group (a workgroup)
   int64_t cells;
   bool joined_inline;
   size_t ml_bytes, o_bytes, need;
@@ -708,8 +991,9 @@ struct AttnPlan {
 AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int max_q, int64_t max_ctx) {
   AttnPlan p;
   const int64_t rows = (int64_t)max_q * (q_heads / heads);
-  p.rt = rows > 16 ? 2 : 1;
-  p.row_groups = (int)((rows + 16 * p.rt - 1) / (16 * p.rt));
+  p.wide = rows > kWideRows;
+  p.group_rows = p.wide ? kWideRows : rows > 16 ? 32 : 16;
+  p.row_groups = (int)((rows + p.group_rows - 1) / p.group_rows);
   p.cells = sequences * heads * p.row_groups;
   const int64_t keys = max_ctx + max_q, unit = kBlock * kWaves;
   // two workgroups to a CU where there are fewer cells; chunks of at most kMaxChunk, so that one long sequence among
@@ -721,10 +1005,10 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   if (splits > kMaxSplits) splits = kMaxSplits;
   p.chunk = (int)((((keys + splits - 1) / splits) + unit - 1) / unit * unit);
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
-  const size_t parts = p.splits > 1 ? (size_t)p.cells * p.splits * 16 * p.rt : 0;
+  const size_t parts = p.splits > 1 ? (size_t)p.cells * p.splits * p.group_rows : 0;
   p.ml_bytes = parts * sizeof(float2);
   p.o_bytes = parts * dim * sizeof(float);
-  p.joined_inline = p.splits > 1 && p.splits <= kInline && p.cells <= kMaxCells;
+  p.joined_inline = !p.wide && p.splits > 1 && p.splits <= kInline && p.cells <= kMaxCells;
   p.need = parts ? kCounterBytes + p.ml_bytes + p.o_bytes : 0;
   return p;
 }
@@ -734,12 +1018,14 @@ void launch(const AttnPlan& p, const AttnArgs& a, int sequences, hipStream_t s) 
   // Chunks vary slowest: workgroups go to the eight XCDs in turn, and the last chunks of a ragged batch are mostly
   // empty.  Row groups of a head, which read the same keys, meet on one XCD where heads are a multiple of 8.
   const dim3 grid(a.c.heads * p.row_groups, sequences, p.splits);
-  if (p.rt == 1)
+  if (p.wide)
+    hipLaunchKernelGGL((tree_attention_wide_kernel<KIND, D>), grid, dim3(256), 0, s, a);
+  else if (p.group_rows == 16)
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 2>), grid, dim3(256), 0, s, a);
   if (p.splits > 1 && !p.joined_inline)
-    hipLaunchKernelGGL((tree_attention_join_kernel<D>), dim3((unsigned)p.cells, 16 * p.rt), dim3(256), 0, s, a, p.splits);
+    hipLaunchKernelGGL((tree_attention_join_kernel<D>), dim3((unsigned)p.cells, p.group_rows), dim3(256), 0, s, a, p.splits);
 }
 
 }  // namespace
@@ -788,7 +1074,7 @@ extern "C" cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_t
                 reinterpret_cast<float2*>(w + kCounterBytes),
                 reinterpret_cast<float*>(w + kCounterBytes + p.ml_bytes),
                 q_token, q_head, tokens, q_heads / cache->heads, table_width, max_q, mask_words, dtype == CL_BF16,
-                p.chunk, p.row_groups, 16 * p.rt, __builtin_ctz(cache->page_size), scale};
+                p.chunk, p.row_groups, p.group_rows, __builtin_ctz(cache->page_size), scale};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (cache->kind == CL_KV_INT8) {
     if (cache->dim == 128)

@@ -138,8 +138,9 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  *   work             device, cl_tree_attention_work_bytes(...) bytes for these arguments, 16-byte aligned (may be
  *                    NULL where that is 0).  Its first CL_ATTENTION_COUNTER_BYTES are zeroed once before its first
  *                    use; calls leave them zeroed.  One call at a time may use it.
- * Scores, maxima, sums and outputs are held in fp32.  The probabilities enter the matrix cores as fp16,
- * scaled so that no value down to 2^-29 of the largest is lost; keys and values enter exactly.
+ * Scores, maxima, sums and outputs are held in fp32; keys and values enter the matrix cores exactly.  The
+ * probabilities (int8: times V's scale) enter them as fp16, scaled so that those down to 2^-24 of the largest
+ * keep fp16's 11 bits; below 2^-35 of it they are lost.
  * A page of block_table outside the cache, or a place past its width, gives NaN in the rows that see it.
  * Sequences whose cu_q does not fit [0, tokens] or max_q are left out (their rows are not written).
  * Deterministic: the same inputs give bitwise identical o.

@@ -80,7 +80,9 @@ def stored(q, s, kind):
 
 # ---------------------------------------------------------------- attention
 def attention(q, k, v, see, scale):
-    """q [t, D], k and v [n, D] float64, see [t, n] -> (o, sum_j p_j |v_j|, largest sum_i |q_i k_i| scale) per row."""
+    """q [t, D], k and v [n, D] float64, see [t, n] -> (o, sum_j p_j |v_j|, largest sum_i |q_i k_i| scale) per row.
+    The second carries 2^-24 of what a probability below fp16's normal range may be off, divided by that 2^-11 with which
+    attention_tolerance weighs it: such a one is kept to 2^-35 of the largest, beside V's scales that differ."""
     s = (q @ k.T) * scale
     s = np.where(see, s, -np.inf)
     m = s.max(-1, keepdims=True, initial=-np.inf)
@@ -88,7 +90,8 @@ def attention(q, k, v, see, scale):
     l = p.sum(-1, keepdims=True)
     p = np.divide(p, l, out=np.zeros_like(p), where=l > 0)
     mag = np.abs(q) @ np.abs(k).T * abs(scale)
-    return p @ v, p @ np.abs(v), np.where(see, mag, 0).max(-1, keepdims=True, initial=0.0)
+    lost = 2.0 ** -24 * p.max(-1, keepdims=True, initial=0.0) * (see @ np.abs(v).max(-1, keepdims=True))
+    return p @ v, p @ np.abs(v) + lost, np.where(see, mag, 0).max(-1, keepdims=True, initial=0.0)
 
 
 def attention_tolerance(o, absv, mag, n, D, dtype):

@@ -161,6 +161,29 @@ def test_trees(case):
 
 
 @pytest.mark.parametrize("kind", ["int8", "int4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("mask,dtype,spread", [("tree", "f16", 0.0), ("random", "bf16", 2.0), ("chain", "f16", 2.0),
+                                               ("none", "bf16", 0.0)])
+def test_many_rows_of_a_kv_head(kind, D, mask, dtype, spread):
+    # up to 520 rows that read the same keys, sequences with fewer rows and keys than the launch was sized for
+    p = Problem([5000, 0, 77, 31, 700], [65, 17, 33, 1, 16], 16, 2, D, 32, kind, dtype, mask=mask, seed=31, spread=spread)
+    say("many rows", kind, D, mask, p.check(p.call()))
+    assert p.torch.equal(p.call(), p.call())
+    clean = p.call()
+    q = p.q.clone()
+    q[2, 1] = float("nan")
+    got = p.call(q=q)
+    assert got[2, 1].isnan().all()
+    got[2, 1] = clean[2, 1]
+    assert p.torch.equal(got, clean)
+    keep = p.table.copy()
+    p.table[0, 3] = p.cache.pages  # in the old tokens of the first sequence: every row sees it
+    got = p.call()
+    p.table = keep
+    assert got[:65].isnan().all() and p.torch.equal(got[65:], clean[65:])
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_long_contexts(kind, dtype):
     p = Problem([9001, 40, 20003], [1, 3, 5], 8, 2, 128, 64, kind, dtype, seed=11)
