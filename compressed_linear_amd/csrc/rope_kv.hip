@@ -1,5 +1,6 @@
 // rope_kv.hip -- rotary positions and the quantised K/V cache: its table,
 // the rotation, appending tokens and reading them back.
+#include <algorithm>
 #include <type_traits>
 
 #include "serving.h"
@@ -140,7 +141,7 @@ struct AppendArgs {
   const int32_t* slots;
   const int32_t* positions;
   const float2* table;  // NULL: no rotation
-  int tokens, rot, layout, table_rows, page_shift;
+  int tokens, rot, layout, table_rows, page_shift, side;
 };
 
 // Eight channels from `at` of a head at x; VEC: as two 16-byte (fp32) or one load, otherwise one by one.
@@ -167,12 +168,14 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// D / 8 lanes a (token, head, k or v), eight channels each; a workgroup has the rows of consecutive tokens of one
-// head, whose scales and, in a page, codes lie together.  Bound by memory for prompts, by the launch for steps.
+// D / 8 lanes a (token, head, k or v), eight channels each; heads side by side in a workgroup as in the read, since the inputs are the
+// larger part of the bytes and a token's heads lie together there (8192 tokens of 32 fp32 heads of 128, rotated, to int8: 71 us
+// with 16 heads, 80 with 4, 83 with one).  Bound by memory for prompts, by the launch for steps.
 template <int IN, int KIND, int D, bool VEC>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   constexpr int LANES = D / 8;
-  const int h = blockIdx.y, which = blockIdx.z, t = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int row_at = threadIdx.x / LANES, h = (blockIdx.y << a.side) + (row_at & ((1 << a.side) - 1)), which = blockIdx.z;
+  const int t = blockIdx.x * (256 / LANES >> a.side) + (row_at >> a.side);
   const int ch = 8 * (threadIdx.x % LANES);
   if (t >= a.tokens) return;
   const int slot = a.slots[t];
@@ -308,6 +311,9 @@ __global__ void __launch_bounds__(256) kv_read_kernel(cl_kv_cache c, int page_sh
   }
 }
 
+// The largest power of two (its logarithm) up to 16 that divides the heads.
+int heads_side_by_side(int heads) { return std::min(__builtin_ctz(heads), 4); }
+
 template <int IN, int OUT>
 void launch_rope(const RopeArgs& a, hipStream_t s) {
   const bool vec = a.rot % 16 == 0 && a.dim % 16 == 0 && aligned_to(a.table, 16) &&
@@ -335,7 +341,8 @@ template <int IN, int KIND, int D>
 void launch_append(const AppendArgs& a, hipStream_t s) {
   const bool vec = heads_aligned(a.src[0], IN, a.token[0], a.head[0]) && heads_aligned(a.src[1], IN, a.token[1], a.head[1]) &&
                    a.rot % 16 == 0;
-  const dim3 grid((unsigned)(((int64_t)a.tokens * (D / 8) + 255) / 256), a.c.heads, 2);
+  const int each = 256 / (D / 8) >> a.side;
+  const dim3 grid((unsigned)(((int64_t)a.tokens + each - 1) / each), a.c.heads >> a.side, 2);
   if (vec)
     hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, true>), grid, dim3(256), 0, s, a);
   else
@@ -360,7 +367,7 @@ void launch_append(const AppendArgs& a, hipStream_t s) {
 template <int OUT, int KIND, int D>
 void launch_read(const cl_kv_cache& c, const int32_t* slots, int n, void* ko, void* vo, hipStream_t s) {
   typedef typename Elem<OUT>::raw raw;
-  const int side = min(__builtin_ctz(c.heads), 4), slots_each = 2 * 256 / (D / 8) >> side;
+  const int side = heads_side_by_side(c.heads), slots_each = 2 * 256 / (D / 8) >> side;
   hipLaunchKernelGGL((kv_read_kernel<OUT, KIND, D>), dim3((unsigned)(((int64_t)n + slots_each - 1) / slots_each), c.heads >> side),
                      dim3(256), 0, s, c, __builtin_ctz(c.page_size), side, slots, n, static_cast<raw*>(ko), static_cast<raw*>(vo));
 }
@@ -473,7 +480,7 @@ extern "C" cl_status cl_kv_append(const cl_kv_cache* cache, const void* k, const
     return fail(CL_EINVAL, "append: a pointer is misaligned for its type");
   if (table && (st = check_rope(positions, table, table_rows, rot, layout, cache->dim)) != CL_OK) return st;
   const AppendArgs a = {*cache, {k, v}, {k_token, v_token}, {k_head, v_head}, slots, positions,
-                        reinterpret_cast<const float2*>(table), tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size)};
+                        reinterpret_cast<const float2*>(table), tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size), heads_side_by_side(cache->heads)};
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)
     launch_append<CL_F16>(a, s);
