@@ -48,8 +48,13 @@ constexpr float kNone = -3.4e38f;  // running maximum before any key
 constexpr float kSlack = 4.f;      // log2 by which a score may pass the running maximum
 constexpr int kProbBits = 11;      // probabilities are scaled by 2^11: with the slack at most 2^15
 
-constexpr int kMaxChunk = 4096;    // keys of a workgroup
-constexpr int kInline = 8;         // chunks that the last workgroup of a cell joins; more are joined by a launch
+// Keys of a workgroup, so that one long sequence among short ones does not run alone at the end (64 sequences of up to 16000
+// tokens, 64 heads over 8: 208 us; 214 with 2048, where the joins cost more, 215 with 8192).
+constexpr int kMaxChunk = 4096;
+// Chunks that the last workgroup of a cell joins; more are joined by a launch of their own, which spreads them over the card
+// (one row of 32 heads, 511 keys in four chunks: 7.7 us, 9.7 with a launch; 64 rows of 8 x 8 heads, 2000 keys in eight: 23.8 and,
+// with a launch, 22.5).
+constexpr int kInline = 4;
 constexpr int kMaxCells = 65536;   // cells (sequence, kv head, row group) that may be joined so: their counters open the workspace
 constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
 
@@ -654,9 +659,16 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
       store(row, x, den == 0.f ? 0.f : 1.f / den);
     } else {
       const int64_t at = (cell * gridDim.z + split) * ROWS + row;
-      if (ch == 0) store_dev2(a.part_ml + at, top, den);
+      float* const op = a.part_o + at * D + ch;
+      if (a.counters) {  // read by a workgroup of this launch
+        if (ch == 0) store_dev2(a.part_ml + at, top, den);
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) store_dev2(reinterpret_cast<float2*>(a.part_o + at * D + ch + j), x[j], x[j + 1]);
+        for (int j = 0; j < 8; j += 2) store_dev2(reinterpret_cast<float2*>(op + j), x[j], x[j + 1]);
+      } else {
+        if (ch == 0) a.part_ml[at] = make_float2(top, den);
+        *reinterpret_cast<f4*>(op) = f4{x[0], x[1], x[2], x[3]};
+        *reinterpret_cast<f4*>(op + 4) = f4{x[4], x[5], x[6], x[7]};
+      }
     }
   }
   if (splits == 1 || !a.counters) return;
@@ -925,8 +937,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a)
 }
 
 // Joins the partial outputs of a row's chunks, in chunk order within each of eight strands and the strands in
-// order: 32 lanes (dim 128) or 16 hold four channels each.  For more than kInline chunks this launch of its own, where
-// as many workgroups as there are rows read the partials, beats one workgroup that reads them all.
+// order: 32 lanes (dim 128) or 16 hold four channels each.
 template <int D>
 __global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, int max_splits) {
   constexpr int LANES = D / 4, STRANDS = 256 / LANES;
@@ -991,16 +1002,25 @@ struct AttnPlan {
 AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int max_q, int64_t max_ctx) {
   AttnPlan p;
   const int64_t rows = (int64_t)max_q * (q_heads / heads);
-  p.wide = rows > kWideRows;
-  p.group_rows = p.wide ? kWideRows : rows > 16 ? 32 : 16;
+  const int64_t keys = max_ctx + max_q, unit = kBlock * kWaves, ones = (keys + unit - 1) / unit;
+  // Rows to a workgroup: more of them read and widen a key once for more rows, but leave fewer workgroups with longer
+  // chains to their end.  128 pay where the keys are cut for want of cells anyway and a CU has 7 steps or more of them (64
+  // tokens of 8 x 8 heads: 16000 keys 67 us against 73 with 32 rows, 4000 keys 37 against 33; 8 such sequences of up to 8000
+  // keys: 216 against 160); 32 where a CU has more than 20 steps of 16 rows (16 tokens of 8 x 8 heads: 16000 keys 30.8 us
+  // against 33.8 with 16 rows, 8000 keys 25.3 against 23.1, 2000 keys 19.4 against 14.6).
+  const auto cells = [&](int r) { return sequences * heads * ((rows + r - 1) / r); };
+  p.wide = rows >= kWideRows && cells(kWideRows) <= 64 && cells(kWideRows) * ones >= 7 * 256;
+  p.group_rows = p.wide ? kWideRows : rows > 16 && cells(16) * ones > 20 * 256 ? 32 : 16;
   p.row_groups = (int)((rows + p.group_rows - 1) / p.group_rows);
-  p.cells = sequences * heads * p.row_groups;
-  const int64_t keys = max_ctx + max_q, unit = kBlock * kWaves;
-  // two workgroups to a CU where there are fewer cells; chunks of at most kMaxChunk, so that one long sequence among
-  // short ones does not run alone at the end
+  p.cells = cells(p.group_rows);
+  // two workgroups to a CU where there are fewer cells (30000 tokens, 64 heads over 8: 21 us; 25 with four)
   int64_t splits = (512 + p.cells - 1) / p.cells;
   if (splits < (keys + kMaxChunk - 1) / kMaxChunk) splits = (keys + kMaxChunk - 1) / kMaxChunk;
-  const int64_t most = (keys + unit - 1) / unit;
+  // Chunks of one step of the four wavefronts where the workgroup that comes last joins 3..kInline of them, else of two steps
+  // or more, since a chunk more costs more than a second step (one row of 32 heads: 200 keys 6.5 us in one chunk and 7.5 in
+  // two, 2000 keys 10.6 in eight and 11.2 in sixteen; but 511 keys 7.7 us in four and 8.5 in two).
+  const int64_t steps = ones > 2 && ones <= kInline ? 1 : 2;
+  const int64_t most = (ones + steps - 1) / steps;
   if (splits > most) splits = most;
   if (splits > kMaxSplits) splits = kMaxSplits;
   p.chunk = (int)((((keys + splits - 1) / splits) + unit - 1) / unit * unit);

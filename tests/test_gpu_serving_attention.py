@@ -184,6 +184,23 @@ def test_many_rows_of_a_kv_head(kind, D, mask, dtype, spread):
 
 
 @pytest.mark.parametrize("kind", ["int8", "int4"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,hq,hkv", [
+    ([4700] + [37 * i % 700 for i in range(23)], [5, 4, 0, 1] * 6, 16, 2),  # up to 40 rows, in groups of 32
+    ([4700] + [0] * 23, [5] + [1] * 23, 16, 2),
+    ([600, 90, 2000], [7, 16, 3], 32, 4),                                   # up to 128, in groups of 16
+    ([3700, 100], [13, 16], 64, 8),                                         # fewer than 128
+    ([29000], [16], 8, 1),                                                  # 128, in groups of 32 or at once
+], ids=["groups32", "groups32-short", "groups16", "many-cells", "long"])
+def test_row_groups(kind, D, ctx, new, hq, hkv):
+    p = Problem(ctx, new, hq, hkv, D, 64, kind, "bf16", mask="tree", seed=41, spread=1.0)
+    say("row groups", kind, D, hq, hkv, p.check(p.call()))
+    assert p.torch.equal(p.call(), p.call())
+    p.check(p.call(max_ctx=0))         # few, long chunks
+    p.check(p.call(max_ctx=10 * max(ctx)))  # more rows to a workgroup than these lengths would get
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_long_contexts(kind, dtype):
     p = Problem([9001, 40, 20003], [1, 3, 5], 8, 2, 128, 64, kind, dtype, seed=11)
