@@ -1109,3 +1109,14 @@ extern "C" cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_t
   }
   return launched("attention");
 }
+
+extern "C" cl_status cl_recording(void* stream, uint64_t* id) {
+  clear_error();
+  if (!id) return fail(CL_EINVAL, "recording: a required pointer is NULL");
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  unsigned long long n = 0;
+  const hipError_t e = hipStreamGetCaptureInfo(static_cast<hipStream_t>(stream), &st, &n);
+  if (e != hipSuccess) return fail(CL_EHIP, "recording: %s", hipGetErrorString(e));
+  *id = st == hipStreamCaptureStatusNone ? 0 : n;
+  return CL_OK;
+}

@@ -11,7 +11,7 @@ import ctypes
 from typing import Optional
 
 SERVING_SYMBOLS = ["cl_rope_table", "cl_rope", "cl_kv_append", "cl_kv_read", "cl_tree_attention_work_bytes",
-                   "cl_tree_attention", "cl_token_logprobs"]
+                   "cl_tree_attention", "cl_recording", "cl_token_logprobs"]
 
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -37,6 +37,7 @@ def declare(L):
     L.cl_tree_attention_work_bytes.argtypes = [i] * 6
     L.cl_tree_attention.argtypes = [p, i, q, q, i, i, cache, p, i, i, p, p, i, i, p, i, ctypes.c_float, p, p,
                                     ctypes.c_size_t, p]
+    L.cl_recording.argtypes = [p, ctypes.POINTER(ctypes.c_uint64)]
     L.cl_token_logprobs.argtypes = [p, i, q, i, i, p, i, p, p, i, p, p, p]
     for name in SERVING_SYMBOLS:
         getattr(L, name).restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
@@ -151,8 +152,9 @@ class KVCache:
 
     Either sizes are given and the cache allocates its tensors, or the four tensors are:
     k, v uint8 [pages, heads, page_size, dim or dim / 2]; k_scale, v_scale float16 [pages, heads,
-    page_size] or [pages, heads, page_size, dim / 32].  It also keeps the attention's workspace: one
-    `tree_attention` at a time per cache.
+    page_size] or [pages, heads, page_size, dim / 32].  It also keeps a workspace of `tree_attention` for
+    each stream it is called on, which a call that is recorded there shares (replays and calls on that stream take
+    turns); one that is recorded where none was called before has a workspace of the recording.
     """
 
     def __init__(self, pages: int = 0, page_size: int = 64, heads: int = 1, dim: int = 128, kind: str = "int8",
@@ -188,8 +190,8 @@ class KVCache:
         self._desc = cl_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page_size,
                                  heads, dim, KV_KIND[kind], 0)
         self._ref = ctypes.byref(self._desc)
-        self._work, self._work_ptr, self._work_bytes = None, None, 0
-        self._outgrown: list = []
+        self._work: dict = {}   # by stream, or stream and recording: address and bytes of the workspace
+        self._keep: list = []   # their tensors, outgrown ones too: a recorded graph may still use them
 
     def append(self, k, v, slots, positions=None, table=None, layout: str = "half"):
         """Quantise new keys and values [tokens, heads, dim] into `slots` (int32 [tokens]; a slot outside the
@@ -230,17 +232,19 @@ class KVCache:
             _check(st, "cl_kv_read")
         return k, v
 
-    def _workspace(self, sizes):
-        """The attention's workspace for these sizes.  One that was outgrown is kept: work on another stream or
-        a recorded graph may still use it."""
+    def _workspace(self, sizes, stream):
+        """Address and bytes of a workspace for these sizes on `stream`.  In a recording it is one of the recording,
+        since what clears it runs with the replays."""
+        recording = ctypes.c_uint64()
+        _check(_lib.cl_recording(stream, ctypes.byref(recording)), "cl_recording")
+        key = (stream, recording.value) if recording.value else stream
         need = _lib.cl_tree_attention_work_bytes(*sizes)
-        if need > self._work_bytes:
-            if self._work is not None:
-                self._outgrown.append(self._work)
-            self._work_bytes = 2 * need
-            self._work = _empty(self._work_bytes, dtype=_torch.uint8, device=self.device)
-            self._work[:COUNTER_BYTES].zero_()  # the calls leave them so
-            self._work_ptr = self._work.data_ptr()
+        if self._work.get(key, (None, 0))[1] < need:
+            work = _empty(2 * need, dtype=_torch.uint8, device=self.device)
+            work[:COUNTER_BYTES].zero_()  # the calls leave them so
+            self._keep.append(work)
+            self._work[key] = work.data_ptr(), 2 * need
+        return self._work[key]
 
 
 def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, max_ctx: Optional[int] = None,
@@ -286,10 +290,9 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
             _index(ctx_lens, B, dev, "ctx_lens"), _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
             1.0 / D ** 0.5 if scale is None else scale, out.data_ptr())
     stream = _stream(dev)
-    st = L.cl_tree_attention(*args, cache._work_ptr, cache._work_bytes, stream)
+    st = L.cl_tree_attention(*args, *cache._work.get(stream, (None, 0)), stream)
     if st == -3:  # the workspace is too small for these sizes: make a larger one, once
-        cache._workspace((B, H, cache.heads, D, max_q, max_ctx))
-        st = L.cl_tree_attention(*args, cache._work_ptr, cache._work_bytes, stream)
+        st = L.cl_tree_attention(*args, *cache._workspace((B, H, cache.heads, D, max_q, max_ctx), stream), stream)
     if st:
         _check(st, "cl_tree_attention")
     return out

@@ -156,6 +156,14 @@ cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_token, int64
                             size_t work_bytes, void* stream);
 
 /*
+ * cl_recording -- the number of the graph recording that `stream` is part of (HIP gives each its own), 0
+ * if it is not recorded.  For callers that keep a workspace to a recording: what clears it runs with the
+ * replays.
+ * Errors: CL_EINVAL (id NULL), CL_EHIP.
+ */
+cl_status cl_recording(void* stream, uint64_t* id);
+
+/*
  * cl_token_logprobs -- log probabilities of given tokens, entropy and top alternatives of each row of
  * logits.  With m = max_j x_j and l = sum_j exp(x_j - m):
  *     logp[t, c] = x[ids[t, c]] - m - log l                     NaN for an id outside [0, vocab)

@@ -290,6 +290,43 @@ def test_other_stream_and_graph():
         assert torch.equal(out, eager), i
 
 
+def test_first_call_recorded():
+    # a cache whose first calls are recorded: their workspaces are cleared by the replays, so nobody else may have them
+    p = Problem([400, 33], [4, 1], 8, 2, 128, 32, "int8", "bf16", seed=18)
+    torch = p.torch
+    want = p.call()
+    tab, ctx, cu = p.dev(p.table), p.dev(p.ctx), p.dev(p.cu)
+    fresh = cla.KVCache(kind="int8", k=p.cache.k, v=p.cache.v, k_scale=p.cache.k_scale, v_scale=p.cache.v_scale)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        out = torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(2):
+                cla.tree_attention(p.q, fresh, tab, ctx, cu, max_q=p.max_q, max_ctx=400, tree_mask=p.mask, out=out)
+        graphs.append((g, out))
+    assert len(fresh._work) == 2
+    with torch.cuda.stream(s):
+        eager = cla.tree_attention(p.q, fresh, tab, ctx, cu, max_q=p.max_q, max_ctx=400, tree_mask=p.mask)
+    s.synchronize()
+    assert torch.equal(eager, want)
+    for _ in range(3):
+        for g, out in reversed(graphs):
+            out.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    for x in (p.cache, fresh):  # a workspace to a stream
+        with torch.cuda.stream(s):
+            got = cla.tree_attention(p.q, x, tab, ctx, cu, max_q=p.max_q, max_ctx=400, tree_mask=p.mask)
+        s.synchronize()
+        assert torch.equal(got, want)
+    assert len({a for a, _ in p.cache._work.values()}) == len(p.cache._work) == 2
+
+
 def test_refusals():
     p = Problem([40], [3], 4, 2, 64, 16, "int8", "f16", seed=9)
     torch = p.torch

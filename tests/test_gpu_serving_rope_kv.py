@@ -220,6 +220,42 @@ def test_slots_past_4_gib():
     assert int((cache.k_scale != 0).sum()) == 3
 
 
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+def test_other_stream_and_graph(kind):
+    torch = torch_cuda()
+    r = np.random.default_rng(77)
+    T, H, D = 37, 4, 128
+    table = cla.rope_table(200, D)
+    k, v = (dev_tensor(r.normal(0, 1, (T, H, D)), "bf16") for _ in range(2))
+    pos, slots = ints(r.integers(0, 200, T)), ints(r.permutation(64)[:T])
+
+    def step(cache, k, v):
+        q = cla.rope(k, pos, table, out_dtype=torch.float16)
+        cache.append(k, v, slots, pos, table)
+        return (q,) + cache.read(slots)
+
+    caches = [cla.KVCache(2, 32, H, D, kind) for _ in range(3)]
+    want = step(caches[0], k, v)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = step(caches[1], k, v)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ki, vi = k.clone(), v.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        out = step(caches[2], ki, vi)
+    for i in range(4):
+        ki.copy_(k * (1.0 + i))
+        vi.copy_(v - i)
+        want = step(caches[0], ki, vi)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
 def test_refusals():
     torch = torch_cuda()
     x = dev_tensor(np.ones((2, 3, 64)))

@@ -118,3 +118,7 @@ def test_logprobs_refusals():
     assert call(k=33) == -2
     assert call(vocab=(1 << 24) + 1) == -5
     assert call(rows=0, x=None) == 0
+
+
+def test_recording_refuses():
+    assert cla.lib().cl_recording(None, None) == -1
