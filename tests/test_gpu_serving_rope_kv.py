@@ -62,6 +62,7 @@ ROPE = [  # T, H, D, rot, layout, in, out
     (2, 3, 7, 6, "half", "bf16", "f32"), (9, 2, 256, 256, "interleaved", "f32", "f32"),
     (130, 9, 96, 96, "half", "bf16", "f16"), (2, 2, 1024, 512, "half", "f16", "bf16"),
     (65, 4, 72, 40, "interleaved", "bf16", "f32"), (300, 80, 128, 128, "half", "f32", "bf16"),
+    (45000, 3, 64, 32, "half", "bf16", "f16"), (18800, 7, 128, 128, "interleaved", "f16", "f32"),  # many tokens, odd heads
 ]
 
 
