@@ -8,10 +8,11 @@ torch's current stream of the tensors' device.  Index tensors are int32.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 SERVING_SYMBOLS = ["cl_rope_table", "cl_rope", "cl_kv_append", "cl_kv_read", "cl_tree_attention_work_bytes",
-                   "cl_tree_attention", "cl_recording", "cl_token_logprobs"]
+                   "cl_tree_attention", "cl_recording", "cl_token_logprobs", "cl_call"]
 
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -39,9 +40,15 @@ def declare(L):
                                     ctypes.c_size_t, p]
     L.cl_recording.argtypes = [p, ctypes.POINTER(ctypes.c_uint64)]
     L.cl_token_logprobs.argtypes = [p, i, q, i, i, p, i, p, p, i, p, p, p]
+    L.cl_call.argtypes = [i, ctypes.c_char_p]
     for name in SERVING_SYMBOLS:
         getattr(L, name).restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
 
+
+# cl_call's entries and how their arguments are packed: 0.2 us a call, where ctypes takes 0.9 for 17 of them
+_ROPE, _APPEND, _READ, _ATTENTION, _LOGPROBS = range(5)
+_pack_rope, _pack_append, _pack_read, _pack_attention, _pack_logprobs = (
+    struct.Struct(f).pack for f in ("17q", "16q", "7q", "16qd4q", "13q"))
 
 _torch = None
 _lib = None
@@ -57,8 +64,9 @@ def _setup():
 
         from . import lib
         _torch, _empty, _i32 = torch, torch.empty, torch.int32
-        _current_device = torch.cuda.current_device
-        # the stream's address without a Stream object around it (1.8 us of a call) where torch has that
+        # the device's number without a check that torch is set up (0.2 us of a call: the tensors are there), the stream's
+        # address without a Stream object around it (1.8 us), where torch has those
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
         _DT.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
@@ -130,7 +138,7 @@ def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None):
     T, H, D = shape
     xt, xh, _ = x.stride()
     if out is None:
-        out = _empty(shape, dtype=out_dtype or x.dtype, device=dev)
+        out = _empty(T, H, D, dtype=out_dtype or x.dtype, device=dev)  # sizes as numbers: 0.8 us less than as a shape
         yt, yh = H * D, D
     else:
         yt, yh, one = out.stride() if out.dim() == 3 else (0, 0, 0)
@@ -139,8 +147,9 @@ def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None):
     if out.dtype not in _DT:
         raise ValueError("the output must be float16, bfloat16 or float32")
     tp, rows, rot = _table(table, dev)
-    st = L.cl_rope(x.data_ptr(), _DT[x.dtype], xt, xh, T, H, D, _index(positions, T, dev, "positions"), tp, rows, rot,
-                   ROPE_LAYOUT[layout], out.data_ptr(), _DT[out.dtype], yt, yh, _stream(dev))
+    st = L.cl_call(_ROPE, _pack_rope(
+        x.data_ptr(), _DT[x.dtype], xt, xh, T, H, D, _index(positions, T, dev, "positions"), tp, rows, rot,
+        ROPE_LAYOUT[layout], out.data_ptr(), _DT[out.dtype], yt, yh, _stream(dev)))
     if st:
         _check(st, "cl_rope")
     return out
@@ -189,7 +198,7 @@ class KVCache:
         self.device = k.device
         self._desc = cl_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page_size,
                                  heads, dim, KV_KIND[kind], 0)
-        self._ref = ctypes.byref(self._desc)
+        self._ref = ctypes.addressof(self._desc)
         self._work: dict = {}   # by stream, or stream and recording: address and bytes of the workspace
         self._keep: list = []   # their tensors, outgrown ones too: a recorded graph may still use them
 
@@ -203,8 +212,7 @@ class KVCache:
                 or shape[1] != self.heads or shape[2] != self.dim:
             raise ValueError(f"k and v must be [tokens, {self.heads}, {self.dim}] of one type on {dev}")
         T = shape[0]
-        pp = tp = None
-        rows = rot = 0
+        pp = tp = rows = rot = 0
         if table is not None:
             tp, rows, rot = _table(table, dev)
             if positions is None:
@@ -212,8 +220,9 @@ class KVCache:
             pp = _index(positions, T, dev, "positions")
         kt, kh, _ = k.stride()
         vt, vh, _ = v.stride()
-        st = _lib.cl_kv_append(self._ref, k.data_ptr(), v.data_ptr(), _DT[dt], T, kt, kh, vt, vh,
-                               _index(slots, T, dev, "slots"), pp, tp, rows, rot, ROPE_LAYOUT[layout], _stream(dev))
+        st = _lib.cl_call(_APPEND, _pack_append(
+            self._ref, k.data_ptr(), v.data_ptr(), _DT[dt], T, kt, kh, vt, vh, _index(slots, T, dev, "slots"), pp, tp,
+            rows, rot, ROPE_LAYOUT[layout], _stream(dev)))
         if st:
             _check(st, "cl_kv_append")
 
@@ -225,9 +234,9 @@ class KVCache:
         if dtype not in _DT:
             raise ValueError("dtype must be float16, bfloat16 or float32")
         n = slots.numel()
-        k, v = _empty((2, n, self.heads, self.dim), dtype=dtype, device=dev).unbind(0)
-        st = _lib.cl_kv_read(self._ref, _index(slots, n, dev, "slots"), n, k.data_ptr(), v.data_ptr(), _DT[dtype],
-                             _stream(dev))
+        k, v = _empty(2, n, self.heads, self.dim, dtype=dtype, device=dev).unbind(0)
+        st = _lib.cl_call(_READ, _pack_read(self._ref, _index(slots, n, dev, "slots"), n, k.data_ptr(), v.data_ptr(),
+                                            _DT[dtype], _stream(dev)))
         if st:
             _check(st, "cl_kv_read")
         return k, v
@@ -239,7 +248,7 @@ class KVCache:
         _check(_lib.cl_recording(stream, ctypes.byref(recording)), "cl_recording")
         key = (stream, recording.value) if recording.value else stream
         need = _lib.cl_tree_attention_work_bytes(*sizes)
-        if self._work.get(key, (None, 0))[1] < need:
+        if self._work.get(key, (0, 0))[1] < need:
             work = _empty(2 * need, dtype=_torch.uint8, device=self.device)
             work[:COUNTER_BYTES].zero_()  # the calls leave them so
             self._keep.append(work)
@@ -274,14 +283,14 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, width]")
     width = block_table.shape[1]
-    words, mp = 0, None
+    words = mp = 0
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.dtype is not _torch.int64 or tree_mask.device != dev \
                 or tree_mask.shape[0] != T or not tree_mask.is_contiguous():
             raise ValueError(f"tree_mask must be a contiguous int64 [{T}, words] tensor on {dev}")
         words, mp = tree_mask.shape[1], tree_mask.data_ptr()
     if out is None:
-        out = _empty(shape, dtype=q.dtype, device=dev)
+        out = _empty(T, H, D, dtype=q.dtype, device=dev)
     elif out.shape != shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and type")
     if max_ctx is None:
@@ -290,9 +299,10 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
             _index(ctx_lens, B, dev, "ctx_lens"), _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
             1.0 / D ** 0.5 if scale is None else scale, out.data_ptr())
     stream = _stream(dev)
-    st = L.cl_tree_attention(*args, *cache._work.get(stream, (None, 0)), stream)
+    st = L.cl_call(_ATTENTION, _pack_attention(*args, *cache._work.get(stream, (0, 0)), stream))
     if st == -3:  # the workspace is too small for these sizes: make a larger one, once
-        st = L.cl_tree_attention(*args, *cache._workspace((B, H, cache.heads, D, max_q, max_ctx), stream), stream)
+        work = cache._workspace((B, H, cache.heads, D, max_q, max_ctx), stream)
+        st = L.cl_call(_ATTENTION, _pack_attention(*args, *work, stream))
     if st:
         _check(st, "cl_tree_attention")
     return out
@@ -322,14 +332,15 @@ def token_logprobs(logits, ids, top_k: int = 0):
     buf = _empty(n + T + 2 * T * max(top_k, 0), dtype=_torch.float32, device=dev)
     at = buf.data_ptr()
     logp, entropy = buf.as_strided((T, C), (C, 1), 0), buf.as_strided((T,), (1,), n)
-    top_ids = top_logp = tip = tlp = None
+    top_ids = top_logp = None
+    tip = tlp = 0
     if top_k > 0:
         top_logp = buf.as_strided((T, top_k), (top_k, 1), n + T)
         top_ids = buf.view(_i32).as_strided((T, top_k), (top_k, 1), n + T + T * top_k)
         tlp = at + 4 * (n + T)
         tip = tlp + 4 * T * top_k
-    st = L.cl_token_logprobs(logits.data_ptr(), dt, row, T, V, ip, C, at, at + 4 * n, top_k, tip, tlp,
-                             _stream(dev))
+    st = L.cl_call(_LOGPROBS, _pack_logprobs(logits.data_ptr(), dt, row, T, V, ip, C, at, at + 4 * n, top_k, tip, tlp,
+                                             _stream(dev)))
     if st:
         _check(st, "cl_token_logprobs")
     return (logp, entropy, top_ids, top_logp) if top_k else (logp, entropy)

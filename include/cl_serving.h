@@ -181,6 +181,15 @@ cl_status cl_token_logprobs(const void* x, int32_t dtype, int64_t x_row, int32_t
                             const int32_t* ids, int32_t given, float* logp, float* entropy, int32_t top_k,
                             int32_t* top_ids, float* top_logp, void* stream);
 
+/*
+ * cl_call -- calls cl_rope, cl_kv_append, cl_kv_read, cl_tree_attention or cl_token_logprobs with its
+ * arguments in an array, in their order: pointers and integers as 64-bit integers, the scale as the bits of a
+ * double.  For bindings that pay for every argument of a foreign call.
+ * Errors: the entry's; CL_EINVAL for an unknown entry or args NULL.
+ */
+enum { CL_CALL_ROPE = 0, CL_CALL_KV_APPEND = 1, CL_CALL_KV_READ = 2, CL_CALL_TREE_ATTENTION = 3, CL_CALL_TOKEN_LOGPROBS = 4 };
+cl_status cl_call(int32_t entry, const int64_t* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -122,3 +122,17 @@ def test_logprobs_refusals():
 
 def test_recording_refuses():
     assert cla.lib().cl_recording(None, None) == -1
+
+
+def test_call_refuses():
+    L = cla.lib()
+    pack = lambda *a: b"".join(int(v).to_bytes(8, "little", signed=True) for v in a)  # noqa: E731
+    assert L.cl_call(0, None) == -1 and L.cl_call(-1, pack(0)) == -1 and L.cl_call(5, pack(0)) == -1
+    # cl_rope: no tokens; dim out of range; heads past 32 bits (which would be 2)
+    ok = [256, 0, 128, 64, 0, 2, 64, 256, 256, 8, 64, 0, 1024, 0, 128, 64, 0]
+    assert L.cl_call(0, pack(*ok)) == 0
+    for at, value in ((6, 2000), (5, 2 ** 32 + 2), (4, -1)):
+        bad = list(ok)
+        bad[at] = value
+        assert L.cl_call(0, pack(*bad)) == (-5 if value == 2000 else -1), at
+        assert L.cl_last_error()
