@@ -4,21 +4,23 @@
 // One pass over a row: a thread takes 32 logits at a time into registers and
 // keeps the running maximum m, l = sum exp(x - m) and w = sum (x - m) exp(x - m)
 // of what it has seen (moving m by d turns w into (w - d l) e^-d, l into
-// l e^-d); threads, wavefronts and, for few rows, workgroups with parts of the row
-// are joined by the same rule.  log p(i) = x_i - m - log l; entropy = log l - w / l.
+// l e^-d); threads and wavefronts are joined by the same rule.  log p(i) = x_i - m - log l; entropy = log l - w / l.
 //
 // Alternatives: logits become 64-bit keys (order of the value, then of the lower id).
-// A tile first finds the top_k-th largest of its lanes' maxima; a logit below that
-// bar, or below an earlier tile's, is none of the top_k, which one float compare
-// settles.  The few that pass are collected in LDS; a wavefront whose list is full
-// keeps its best top_k, whose last then is an exact bar (rows of equal or mostly masked
+// With k wanted of W wavefronts, each wavefront names the ceil(k / W)-th largest of its lanes' maxima, and the
+// ceil(k / that)-th largest of those is a bar that k logits reach.  What is below the bar, or below a wavefront's own one
+// in a later tile, is none of the k, which one vote for most tiles, one for each four logits of a lane and one for each
+// logit settle.  The few that pass are collected in LDS; a wavefront whose list is full
+// keeps its best k, whose last then is an exact bar (rows of equal or mostly masked
 // logits).  At the end the candidates above the highest bar of the workgroup are ranked by
 // counting the larger ones: keys are unique, so a rank is a place in the output.
 //
 // Bound by the read of the logits where there are rows for the whole card (4096 rows of
-// 32000 fp32 logits with 4 given tokens and 5 alternatives: 96 us, 5.4 TB/s); a single
-// row by one CU's vector instructions and the latency of the joins (32000 logits, 8
-// alternatives: 9.2 us; spread over eight workgroups that meet at a counter 10.4).
+// 32000 fp32 logits with 4 given tokens and 5 alternatives: 98 us, 5.3 TB/s); a single
+// row by the latency of loads, votes and joins (32000 logits, 8 alternatives: 6.9 us, without alternatives 4.9; spread
+// over eight workgroups that meet at a counter it took a microsecond more).
+#include <type_traits>
+
 #include "serving.h"
 
 namespace cl {
@@ -65,9 +67,37 @@ __device__ __forceinline__ void join(Stat& a, const Stat& b) {
   a.l = ea * a.l + eb * b.l;
   a.m = m;
 }
+
+// Reductions over a wavefront by lane permutes (rows of 16 lanes, then the four rows); every lane gets the same bits.
+template <int CTRL>
+__device__ __forceinline__ uint32_t permuted(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+template <typename F>
+__device__ __forceinline__ uint32_t reduced(uint32_t v, F f) {
+  v = f(v, permuted<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = f(v, permuted<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = f(v, permuted<0x141>(v));  // row_half_mirror
+  v = f(v, permuted<0x140>(v));  // row_mirror
+  const auto row = [&](int r) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * r); };
+  return f(f(row(0), row(1)), f(row(2), row(3)));
+}
+__device__ __forceinline__ float max_of_lanes(float v) {
+  const auto f = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  };
+  return __builtin_bit_cast(float, reduced(__builtin_bit_cast(uint32_t, v), f));
+}
+__device__ __forceinline__ float sum_of_lanes(float v) {
+  const auto f = [](uint32_t a, uint32_t b) {
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+  };
+  return __builtin_bit_cast(float, reduced(__builtin_bit_cast(uint32_t, v), f));
+}
 __device__ __forceinline__ void join_lanes(Stat& a) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) join(a, Stat{__shfl_xor(a.m, d), __shfl_xor(a.l, d), __shfl_xor(a.w, d)});
+  join(a, Stat{max_of_lanes(a.m), 0.f, 0.f});
+  a.l = sum_of_lanes(a.l);
+  a.w = sum_of_lanes(a.w);
 }
 
 constexpr int kList = 128;  // candidates of a wavefront
@@ -133,42 +163,55 @@ struct Best {
   static __device__ __forceinline__ void lds_ordered() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 };
 
-// A row's logits [0, j1), by a workgroup of kThreads.
-template <int DT, bool VEC, int kThreads>
-__device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ x, int j1, Stat& st, Best& best) {
-  constexpr int kTile = kThreads * kPer;
+// The n-th largest of the lanes' `u`, rounded down to its upper half, found from the highest bit down.
+__device__ __forceinline__ uint32_t nth_of_lanes(uint32_t u, int n) {
+  if (n == 1) return reduced(u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  uint32_t at_least = 0;
+  for (int bit = 31; bit >= 16; --bit) {
+    const uint32_t to = at_least | 1u << bit;
+    if (__builtin_popcountll(__ballot(u >= to)) >= n) at_least = to;
+  }
+  return at_least;
+}
+
+// A row's logits [0, n), by a workgroup of kThreads, from the 16-byte boundary at or before its start.
+template <int DT, int kThreads>
+__device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ x, int n, Stat& st, Best& best) {
   typedef typename Elem<DT>::raw raw;
-  constexpr int V = VEC ? 16 / (int)sizeof(raw) : 1;  // logits of a load
-  const int tid = threadIdx.x;
+  constexpr int kTile = kThreads * kPer, kWaves = kThreads / 64;
+  constexpr int V = 16 / (int)sizeof(raw);  // logits of a load
+  __shared__ uint32_t s_bar[kWaves];
+  const int tid = threadIdx.x, before = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(raw));
   st = Stat{-INFINITY, 0.f, 0.f};
-  for (int t0 = 0; t0 < j1; t0 += kTile) {
+  for (int t0 = -before; t0 < n; t0 += kTile) {
     float v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer / V; ++i) {
       const int j = t0 + (i * kThreads + tid) * V;
-      if constexpr (VEC) {
-        uint4 r = {0, 0, 0, 0};
-        if (j + V <= j1) {
-          r = *reinterpret_cast<const uint4*>(x + j);
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      if (j >= 0 && j + V <= n) {
+        const uint4 r = *reinterpret_cast<const uint4*>(x + j);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            if constexpr (DT == CL_F32)
-              v[i * V + e] = __builtin_bit_cast(float, w[e]);
-            else
-              v[i * V + e] = Elem<DT>::up((uint16_t)(w[e / 2] >> (16 * (e % 2))));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) v[i * V + e] = j + e < j1 ? Elem<DT>::up(x[j + e]) : -INFINITY;
+        for (int e = 0; e < V; ++e) {
+          if constexpr (DT == CL_F32)
+            v[i * V + e] = __builtin_bit_cast(float, w[e]);
+          else
+            v[i * V + e] = Elem<DT>::up((uint16_t)(w[e / 2] >> (16 * (e % 2))));
         }
       } else {
-        v[i] = j < j1 ? Elem<DT>::up(x[j]) : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i * V + e] = j + e >= 0 && j + e < n ? Elem<DT>::up(x[j + e]) : -INFINITY;
       }
     }
-    float top = v[0];
+    constexpr int kGroup = 4, kGroups = kPer / kGroup;
+    float g[kGroups], peak, top;  // largest of each four and of all, a NaN if there is one; largest without the fours that have one
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) top = fmaxf(top, v[i]);
+    for (int i = 0; i < kGroups; ++i) {
+      g[i] = __builtin_elementwise_maximum(__builtin_elementwise_maximum(v[kGroup * i], v[kGroup * i + 1]),
+                                           __builtin_elementwise_maximum(v[kGroup * i + 2], v[kGroup * i + 3]));
+      peak = i ? __builtin_elementwise_maximum(peak, g[i]) : g[i];
+      top = i ? fmaxf(top, g[i]) : g[i];
+    }
     // sums
     const float m = fmaxf(st.m, top);
     join(st, Stat{m, 0.f, 0.f});
@@ -184,30 +227,41 @@ __device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ 
     st.w += w;
     // alternatives
     if (best.k) {
-      if (__builtin_popcountll(__ballot(top > best.bar)) > best.k) {
-        // the k-th largest of the lanes' maxima, found from its highest bit down (and rounded down: 20 bits are enough)
-        uint32_t u = __builtin_bit_cast(uint32_t, top + 0.0f), at_least = 0;
-        u = top != top ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
-        for (int bit = 31; bit >= 12; --bit) {
-          const uint32_t to = at_least | 1u << bit;
-          if (__builtin_popcountll(__ballot(u >= to)) >= best.k) at_least = to;
-        }
-        best.bar = fmaxf(best.bar, key_value((u64)at_least << 32));
-      }
+      uint32_t u = __builtin_bit_cast(uint32_t, top + 0.0f);
+      u = top != top ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
+      if (t0 <= 0) {
+        // where `enough` wavefronts have `each` lanes whose maxima reach a value, top_k logits do: the value is the enough-th
+        // largest of their each-th largest
+        const int each = (best.k + kWaves - 1) / kWaves, enough = (best.k + each - 1) / each;
+        const uint32_t own = nth_of_lanes(u, each);
+        if (tid % 64 == 0) s_bar[tid / 64] = own;
+        __syncthreads();
+        const uint32_t mine = s_bar[tid % kWaves];
+        int reach = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const u64 who = __ballot(!(v[i] < best.bar));  // a NaN passes
-        if (who) {
-          const int j = t0 + (i / V * kThreads + tid) * V + i % V;
-          best.add(rank_key(v[i], j), who & __ballot(j < j1));
+        for (int i = 0; i < kWaves; ++i) reach += s_bar[i] >= mine;
+        best.bar = fmaxf(best.bar, key_value((u64)nth_of_lanes(reach >= enough ? mine : 0, 1) << 32));
+      }
+      if (__builtin_popcountll(__ballot(top > best.bar)) > best.k)
+        best.bar = fmaxf(best.bar, key_value((u64)nth_of_lanes(u, best.k) << 32));
+      if (!__any(!(peak < best.bar))) continue;
+#pragma unroll
+      for (int f = 0; f < kGroups; ++f) {
+        if (!__any(!(g[f] < best.bar))) continue;
+#pragma unroll
+        for (int i = kGroup * f; i < kGroup * f + kGroup; ++i) {
+          const u64 who = __ballot(!(v[i] < best.bar));  // a NaN passes
+          if (who) {
+            const int j = t0 + (i / V * kThreads + tid) * V + i % V;
+            best.add(rank_key(v[i], j), who & __ballot(j >= 0 && j < n));
+          }
         }
       }
     }
   }
 }
 
-// Joins the wavefronts' sums.  A join is not the same to the last bit from both its sides, so every lane takes
-// lane 0's result.
+// Joins the wavefronts' sums.
 template <int kWaves>
 __device__ __forceinline__ void join_waves(Stat& st) {
   __shared__ float s_st[kWaves][3];
@@ -217,14 +271,10 @@ __device__ __forceinline__ void join_waves(Stat& st) {
   __syncthreads();
   st = lane < kWaves ? Stat{s_st[lane][0], s_st[lane][1], s_st[lane][2]} : Stat{-INFINITY, 0.f, 0.f};
   join_lanes(st);
-  const auto lane0 = [](float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
-  };
-  st = Stat{lane0(st.m), lane0(st.l), lane0(st.w)};
 }
 
 // One workgroup a row.
-template <int DT, bool VEC, int kThreads>
+template <int DT, int kThreads>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
   constexpr int kWaves = kThreads / 64;
   __shared__ u64 s_list[kWaves * kList], s_all[kWaves * kList];
@@ -232,17 +282,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
   __shared__ int s_n;
   const int t = blockIdx.x, tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const auto* x = static_cast<const typename Elem<DT>::raw*>(a.x) + t * a.x_row;
-  // the first given tokens' logits are asked for at once
-  float mine = __builtin_nanf("");
-  if (tid < a.given) {
-    const int id = a.ids[(int64_t)t * a.given + tid];
-    if (id >= 0 && id < a.vocab) mine = Elem<DT>::up(x[id]);
-  }
+  const int first = tid < a.given ? a.ids[(int64_t)t * a.given + tid] : -1;
   if (tid == 0) s_n = 0;
   Stat st;
   Best best;
   best.clear(s_list + wave * kList, a.top_k);
-  scan<DT, VEC, kThreads>(x, a.vocab, st, best);
+  scan<DT, kThreads>(x, a.vocab, st, best);
+  // the first given tokens' logits fly while the sums are joined
+  float mine = __builtin_nanf("");
+  if (first >= 0 && first < a.vocab) mine = Elem<DT>::up(x[first]);
   if (lane == 0) s_bar[wave] = best.bar;
   join_waves<kWaves>(st);  // a barrier: bars and the cleared count are there
   const float lse = __builtin_amdgcn_logf(st.l) * kLn2;
@@ -278,22 +326,24 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
   }
 }
 
-template <int DT, int kThreads>
-void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
-  if (vec)
-    hipLaunchKernelGGL((logprobs_kernel<DT, true, kThreads>), dim3(rows), dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((logprobs_kernel<DT, false, kThreads>), dim3(rows), dim3(kThreads), 0, s, a);
-}
-
 template <int DT>
-void launch_logprobs(const LogprobArgs& a, int rows, bool vec, hipStream_t s) {
-  // Sixteen wavefronts a row while the rows leave CUs free (256 x 32000: 13.2 against 18.1 us; 384: 21.4 against
-  // 19.4); four for more rows, or where they hold a row in one tile (256 x 5000: 7.3 against 10.0).
-  if (rows > 256 || a.vocab <= 256 * kPer)
-    launch_logprobs<DT, 256>(a, rows, vec, s);
+void launch_logprobs(const LogprobArgs& a, int rows, hipStream_t s) {
+  const auto go = [&](auto threads) {
+    constexpr int n = decltype(threads)::value;
+    hipLaunchKernelGGL((logprobs_kernel<DT, n>), dim3(rows), dim3(n), 0, s, a);
+  };
+  // Four wavefronts a row where they hold it in one tile (5000 logits, 512 rows: 7.9 us; eight 9.3, sixteen 15) or where rows
+  // abound (32000, 4096 rows: 99.6; 100.4, 142); more while rows leave CUs free or are long: sixteen for up to 256 rows
+  // (32000: 12.0; 13.1 with eight, 17.6 with four) unless eight hold the row (12000: 7.8; 8.8 with sixteen) and for long ones
+  // (151937, 1024 rows: 120; 131, 144), eight between (32000, 512 rows: 16.7; 20.6 with four, 20.7 with sixteen).
+  if (a.vocab <= 256 * kPer)
+    go(std::integral_constant<int, 256>());
+  else if (rows <= 256 ? a.vocab > 512 * kPer : a.vocab > 65536)
+    go(std::integral_constant<int, 1024>());
+  else if (rows <= 512)
+    go(std::integral_constant<int, 512>());
   else
-    launch_logprobs<DT, 1024>(a, rows, vec, s);
+    go(std::integral_constant<int, 256>());
 }
 
 }  // namespace
@@ -315,14 +365,12 @@ extern "C" cl_status cl_token_logprobs(const void* x, int32_t dtype, int64_t x_r
     return fail(CL_EINVAL, "logprobs: a required pointer is NULL");
   if (!aligned_to(x, elem_size(dtype))) return fail(CL_EINVAL, "logprobs: x is misaligned for its type");
   const LogprobArgs a = {x, x_row, ids, logp, entropy, top_ids, top_logp, vocab, given, top_k};
-  // 16-byte loads where every row starts on a 16-byte boundary
-  const bool vec = aligned_to(x, 16) && (x_row * (int64_t)elem_size(dtype)) % 16 == 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)
-    launch_logprobs<CL_F16>(a, rows, vec, s);
+    launch_logprobs<CL_F16>(a, rows, s);
   else if (dtype == CL_BF16)
-    launch_logprobs<CL_BF16>(a, rows, vec, s);
+    launch_logprobs<CL_BF16>(a, rows, s);
   else
-    launch_logprobs<CL_F32>(a, rows, vec, s);
+    launch_logprobs<CL_F32>(a, rows, s);
   return launched("logprobs");
 }
