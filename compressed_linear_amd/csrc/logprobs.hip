@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
   for (int i = tid / 16; i < n; i += kThreads / 16) {  // 16 lanes a candidate
     const u64 key = s_all[i];
     int at = 0;
+#pragma unroll 8
     for (int j = tid % 16; j < n; j += 16) at += s_all[j] > key;
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) at += __shfl_xor(at, d);
