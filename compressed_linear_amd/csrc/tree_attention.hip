@@ -26,7 +26,7 @@
 // wavefront a step), so that the output is rarely rescaled.
 //
 // The keys of a sequence are cut into chunks, a workgroup each, whose four
-// wavefronts take every fourth block of 32 keys; the partial outputs of a few
+// wavefronts (one where there are many cells of few keys) take every fourth block of 32 keys; the partial outputs of a few
 // chunks are joined by the workgroup that finishes last, those of many by a second,
 // small launch, in either case in chunk order.
 //
@@ -61,6 +61,7 @@ constexpr int kMaxChunk = 4096;
 // (one row of 32 heads, 511 keys in four chunks: 7.7 us, 9.7 with a launch; 64 rows of 8 x 8 heads, 2000 keys in eight: 23.8 and,
 // with a launch, 22.5).
 constexpr int kInline = 4;
+constexpr int kFewKeys = 256;      // up to which many cells are a wavefront each
 constexpr int kMaxCells = 65536;   // cells (sequence, kv head, row group) that may be joined so: their counters open the workspace
 constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
 
@@ -376,8 +377,8 @@ __device__ __forceinline__ void wait_lds() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-template <int KIND, int D, int RT>
-__global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
+template <int KIND, int D, int RT, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 2) tree_attention_kernel(AttnArgs a) {
   constexpr int STEPS = D / 32;  // matrix-core steps of a score tile
   constexpr int CB = D / 16;     // channel blocks of the output; lane c of a block's 16 rows is channel CB c + block
   constexpr int ROWS = 16 * RT, STRIDE = D + 4;
@@ -386,10 +387,10 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   constexpr int PIECES = ROWB / 16, TILEB = 16 * ROWB;
   // a block of K and V of each wavefront, and later its output
   constexpr int BLOCKB = 4 * TILEB;
-  constexpr size_t KVBYTES = (size_t)kWaves * BLOCKB, OBYTES = (size_t)kWaves * ROWS * STRIDE * 4;
+  constexpr size_t KVBYTES = (size_t)WAVES * BLOCKB, OBYTES = (size_t)WAVES * ROWS * STRIDE * 4;
   __shared__ __align__(1024) uint8_t s_mem[KVBYTES > OBYTES ? KVBYTES : OBYTES];
   float (*const s_o)[ROWS][STRIDE] = reinterpret_cast<float (*)[ROWS][STRIDE]>(s_mem);
-  __shared__ float2 s_ml[kWaves][ROWS];
+  __shared__ float2 s_ml[WAVES][ROWS];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63, c16 = l & 15, g = l >> 4;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   // pages of the wavefront's next 64 tiles of 16 keys, one to a lane: -1 outside the cache or the table
   int pages = 0;
   const auto load_pages = [&](uint32_t from, int i) {
-    const uint32_t at = from + (uint32_t)(wave + kWaves * (i + (l >> 1))) * kBlock + 16 * (l & 1);
+    const uint32_t at = from + (uint32_t)(wave + WAVES * (i + (l >> 1))) * kBlock + 16 * (l & 1);
     const uint32_t col = at >> a.page_shift;
     int p = col < (uint32_t)a.table_width ? a.block_table[(int64_t)b * a.table_width + col] : -1;
     pages = p < a.c.pages ? p : -1;
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   // Row of the cache where tile t of step i starts.  A tile past the sequence's end, or without a page, is read
   // from page 0, which is there; its keys are masked, or the rows that see them become NaN.
   const auto row_of = [&](int i, int t, int* bad) -> int64_t {
-    const int blk = wave + kWaves * i;
+    const int blk = wave + WAVES * i;
     const uint32_t at = k0 + (uint32_t)blk * kBlock + 16 * t;
     int page = __builtin_amdgcn_readlane(pages, 2 * (i & 31) + t);
     if (blk >= blocks || at >= n) {
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   };
 
   // ---- the first block and raw Q
-  const int steps = wave < blocks ? (blocks - wave + kWaves - 1) / kWaves : 0;
+  const int steps = wave < blocks ? (blocks - wave + WAVES - 1) / WAVES : 0;
   Scales<KIND> sc_next;
   int bad_next = 0;
   if (steps > 0) bad_next = load(0, sc_next);
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
     const Scales<KIND> sc = sc_next;
     const int bad = bad_next;
     if (i + 1 < steps) bad_next = load(i + 1, sc_next);
-    const uint32_t j0 = k0 + (uint32_t)(wave + kWaves * i) * kBlock;
+    const uint32_t j0 = k0 + (uint32_t)(wave + WAVES * i) * kBlock;
     const int left = (int)min(n - j0, (uint32_t)kBlock);         // keys of the block that exist
     const bool special = j0 + kBlock > (uint32_t)ctx || bad;     // some rows may not see some keys
 
@@ -650,12 +651,12 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
     uint16_t* op = a.o + ((int64_t)(first + at / G) * (a.c.heads * G) + hk * G + at % G) * D + ch;
     *reinterpret_cast<u4*>(op) = u4{w[0], w[1], w[2], w[3]};
   };
-  for (int row = tid / PARTS; row < rows; row += 256 / PARTS) {
-    float top = kNone, w[kWaves], den = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int row = tid / PARTS; row < rows; row += 64 * WAVES / PARTS) {
+    float top = kNone, w[WAVES], den = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) top = fmaxf(top, s_ml[v][row].x);
+    for (int v = 0; v < WAVES; ++v) top = fmaxf(top, s_ml[v][row].x);
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
+    for (int v = 0; v < WAVES; ++v) {
       w[v] = __builtin_amdgcn_exp2f(s_ml[v][row].x - top);
       den += w[v] * s_ml[v][row].y;
 #pragma unroll
@@ -688,7 +689,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_kernel(AttnArgs a) {
   }
   __syncthreads();
   if (!s_last) return;
-  for (int row = tid / PARTS; row < rows; row += 256 / PARTS) {
+  for (int row = tid / PARTS; row < rows; row += 64 * WAVES / PARTS) {
     float mv[kInline], lv[kInline], x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, top = kNone, den = 0.f;
     float2 part[kInline][4];
 #pragma unroll
@@ -904,15 +905,15 @@ __global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a)
         for (int j = 0; j < 4; ++j) ks[4 * t + j] = k4[j], vs[4 * t + j] = v4[j];
       }
     }
-    u4 vf[CB];  // V's operands, asked for before the softmax
+    u4 vf[CB - 2];  // V's operands, asked for before the softmax as far as there are registers
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb) vf[cb] = *reinterpret_cast<const u4*>(vt + (16 * cb + c16) * VS + 16 * g);
+    for (int cb = 0; cb < CB - 2; ++cb) vf[cb] = *reinterpret_cast<const u4*>(vt + (16 * cb + c16) * VS + 16 * g);
     uint32_t p[RT][4];
     finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs);
     probabilities<KIND>(s, vs, st, o, p);
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
-      const u4 w = vf[cb];
+      const u4 w = cb < CB - 2 ? vf[cb < CB - 2 ? cb : 0] : *reinterpret_cast<const u4*>(vt + (16 * cb + c16) * VS + 16 * g);
       const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int r = 0; r < RT; ++r) o[r][cb] = mfma16(v, p[r], o[r][cb]);
@@ -1003,6 +1004,7 @@ __global__ void __launch_bounds__(256) tree_attention_join_kernel(AttnArgs a, in
 struct AttnPlan {
   bool wide;
   int group_rows, row_groups, splits, chunk;  // rows of a row group (a workgroup)
+  int waves;                                  // wavefronts of one of 16 rows
   int64_t cells;
   bool joined_inline;
   size_t ml_bytes, o_bytes, need;
@@ -1016,10 +1018,11 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   // chains to their end.  128 pay where the keys are cut for want of cells anyway and a CU has 7 steps or more of them (64
   // tokens of 8 x 8 heads: 16000 keys 67 us against 73 with 32 rows, 4000 keys 37 against 33; 8 such sequences of up to 8000
   // keys: 216 against 160); 32 where a CU has more than 20 steps of 16 rows (16 tokens of 8 x 8 heads: 16000 keys 30.8 us
-  // against 33.8 with 16 rows, 8000 keys 25.3 against 23.1, 2000 keys 19.4 against 14.6).
+  // against 33.8 with 16 rows, 8000 keys 25.3 against 23.1, 2000 keys 19.4 against 14.6), unless the keys are few (26 x 60 tokens
+  // over 60: 27 us with 32 rows, 20 with 16 and one wavefront).
   const auto cells = [&](int r) { return sequences * heads * ((rows + r - 1) / r); };
   p.wide = rows >= kWideRows && cells(kWideRows) <= 64 && cells(kWideRows) * ones >= 7 * 256;
-  p.group_rows = p.wide ? kWideRows : rows > 16 && cells(16) * ones > 20 * 256 ? 32 : 16;
+  p.group_rows = p.wide ? kWideRows : rows > 16 && keys > kFewKeys && cells(16) * ones > 20 * 256 ? 32 : 16;
   p.row_groups = (int)((rows + p.group_rows - 1) / p.group_rows);
   p.cells = cells(p.group_rows);
   // two workgroups to a CU where there are fewer cells (30000 tokens, 64 heads over 8: 21 us; 25 with four)
@@ -1034,6 +1037,10 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   if (splits > kMaxSplits) splits = kMaxSplits;
   p.chunk = (int)((((keys + splits - 1) / splits) + unit - 1) / unit * unit);
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
+  // One wavefront where a cell is one block of keys, or where few keys meet more cells than the card holds workgroups of four:
+  // a small workgroup's chain is as long as a large one's, and four times as many run (64 x 52 heads of one row: 100 keys 18 us
+  // against 27, 250 keys of 60 x 52 17 against 22, but 1000 keys 92 against 82; 64 x 8 heads: 120 keys 9.1 against 8.3).
+  p.waves = p.group_rows == 16 && p.splits == 1 && (keys <= kBlock || (p.cells > 1024 && keys <= kFewKeys)) ? 1 : kWaves;
   const size_t parts = p.splits > 1 ? (size_t)p.cells * p.splits * p.group_rows : 0;
   p.ml_bytes = parts * sizeof(float2);
   p.o_bytes = parts * dim * sizeof(float);
@@ -1049,10 +1056,12 @@ void launch(const AttnPlan& p, const AttnArgs& a, int sequences, hipStream_t s) 
   const dim3 grid(a.c.heads * p.row_groups, sequences, p.splits);
   if (p.wide)
     hipLaunchKernelGGL((tree_attention_wide_kernel<KIND, D>), grid, dim3(256), 0, s, a);
+  else if (p.waves == 1)
+    hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1, 1>), grid, dim3(64), 0, s, a);
   else if (p.group_rows == 16)
-    hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 1, kWaves>), grid, dim3(64 * kWaves), 0, s, a);
   else
-    hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 2>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((tree_attention_kernel<KIND, D, 2, kWaves>), grid, dim3(64 * kWaves), 0, s, a);
   if (p.splits > 1 && !p.joined_inline)
     hipLaunchKernelGGL((tree_attention_join_kernel<D>), dim3((unsigned)p.cells, p.group_rows), dim3(256), 0, s, a, p.splits);
 }

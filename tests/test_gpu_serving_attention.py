@@ -191,7 +191,10 @@ def test_many_rows_of_a_kv_head(kind, D, mask, dtype, spread):
     ([600, 90, 2000], [7, 16, 3], 32, 4),                                   # up to 128, in groups of 16
     ([3700, 100], [13, 16], 64, 8),                                         # fewer than 128
     ([29000], [16], 8, 1),                                                  # 128, in groups of 32 or at once
-], ids=["groups32", "groups32-short", "groups16", "many-cells", "long"])
+    ([20, 31, 0, 5, 17], [1, 1, 2, 3, 1], 8, 4),                            # a wavefront each: one block of keys
+    ([200 - 5 * i for i in range(40)], [1 + i % 5 for i in range(40)], 64, 32),  # the same: many cells of few keys
+    ([60] * 18, [17, 9, 30] * 6, 64, 8),
+], ids=["groups32", "groups32-short", "groups16", "many-cells", "long", "one-block", "few-keys", "few-keys-rows"])
 def test_row_groups(kind, D, ctx, new, hq, hkv):
     p = Problem(ctx, new, hq, hkv, D, 64, kind, "bf16", mask="tree", seed=41, spread=1.0)
     say("row groups", kind, D, hq, hkv, p.check(p.call()))
