@@ -1015,13 +1015,14 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   const int64_t rows = (int64_t)max_q * (q_heads / heads);
   const int64_t keys = max_ctx + max_q, unit = kBlock * kWaves, ones = (keys + unit - 1) / unit;
   // Rows to a workgroup: more of them read and widen a key once for more rows, but leave fewer workgroups with longer
-  // chains to their end.  128 pay where the keys are cut for want of cells anyway and a CU has 7 steps or more of them (64
-  // tokens of 8 x 8 heads: 16000 keys 67 us against 73 with 32 rows, 4000 keys 37 against 33; 8 such sequences of up to 8000
-  // keys: 216 against 160); 32 where a CU has more than 20 steps of 16 rows (16 tokens of 8 x 8 heads: 16000 keys 30.8 us
+  // chains to their end.  128 pay for one sequence, whose keys are cut evenly, where a CU has 7 steps or more of them (64
+  // tokens of 8 x 8 heads: 16000 keys 67 us against 73 with 32 rows, 4000 keys 37 against 33), not for several, whose
+  // lengths differ (8 such sequences of up to 8000 keys: 173 against 100; two of up to 30000: 189 against 201, of 8000 70 against
+  // 65); 32 where a CU has more than 20 steps of 16 rows (16 tokens of 8 x 8 heads: 16000 keys 30.8 us
   // against 33.8 with 16 rows, 8000 keys 25.3 against 23.1, 2000 keys 19.4 against 14.6), unless the keys are few (26 x 60 tokens
   // over 60: 27 us with 32 rows, 20 with 16 and one wavefront).
   const auto cells = [&](int r) { return sequences * heads * ((rows + r - 1) / r); };
-  p.wide = rows >= kWideRows && cells(kWideRows) <= 64 && cells(kWideRows) * ones >= 7 * 256;
+  p.wide = rows >= kWideRows && sequences == 1 && cells(kWideRows) * ones >= 7 * 256;
   p.group_rows = p.wide ? kWideRows : rows > 16 && keys > kFewKeys && cells(16) * ones > 20 * 256 ? 32 : 16;
   p.row_groups = (int)((rows + p.group_rows - 1) / p.group_rows);
   p.cells = cells(p.group_rows);

@@ -185,6 +185,28 @@ def test_many_rows_of_a_kv_head(kind, D, mask, dtype, spread):
 
 @pytest.mark.parametrize("kind", ["int8", "int4"])
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,hint,mask,dtype,spread", [
+    (29000, 64, 29000, "tree", "bf16", 0.0), (5000, 65, 120000, "random", "f16", 2.0), (0, 200, 100000, "random", "bf16", 0.0),
+    (77, 16, 250000, "chain", "f16", 2.0), (700, 33, 100000, "none", "bf16", 2.0)])
+def test_many_rows_of_one_sequence(kind, D, ctx, new, hint, mask, dtype, spread):
+    # 128 rows to a workgroup; a hint that is too long sizes the launch as if the sequence were
+    p = Problem([ctx], [new], 16, 2, D, 32, kind, dtype, mask=mask, seed=37, spread=spread)
+    clean = p.call(max_ctx=hint)
+    say("many rows of one", kind, D, ctx, new, p.check(clean))
+    assert p.torch.equal(p.call(max_ctx=hint), clean)
+    q = p.q.clone()
+    q[2, 1] = float("nan")
+    got = p.call(q=q, max_ctx=hint)
+    assert got[2, 1].isnan().all()
+    got[2, 1] = clean[2, 1]
+    assert p.torch.equal(got, clean)
+    if ctx >= 77:
+        p.table[0, 1] = p.cache.pages  # in the old tokens: every row sees it
+        assert p.call(max_ctx=hint).isnan().all()
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ctx,new,hq,hkv", [
     ([4700] + [37 * i % 700 for i in range(23)], [5, 4, 0, 1] * 6, 16, 2),  # up to 40 rows, in groups of 32
     ([4700] + [0] * 23, [5] + [1] * 23, 16, 2),
