@@ -313,14 +313,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a) {
   }
   __syncthreads();
   const int n = s_n;
-  for (int i = tid / 16; i < n; i += kThreads / 16) {  // 16 lanes a candidate
+  for (int i = tid; i < n; i += kThreads) {
     const u64 key = s_all[i];
-    int at = 0;
-#pragma unroll 8
-    for (int j = tid % 16; j < n; j += 16) at += s_all[j] > key;
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) at += __shfl_xor(at, d);
-    if (tid % 16 == 0 && at < a.top_k) {
+    const int at = rank_in(s_all, n, key);
+    if (at < a.top_k) {
       a.top_ids[(int64_t)t * a.top_k + at] = (int)~(uint32_t)key;
       a.top_logp[(int64_t)t * a.top_k + at] = key_value(key) - st.m - lse;
     }
@@ -333,11 +329,17 @@ void launch_logprobs(const LogprobArgs& a, int rows, hipStream_t s) {
     constexpr int n = decltype(threads)::value;
     hipLaunchKernelGGL((logprobs_kernel<DT, n>), dim3(rows), dim3(n), 0, s, a);
   };
-  // Four wavefronts a row where they hold it in one tile (5000 logits, 512 rows: 7.9 us; eight 9.3, sixteen 15) or where rows
-  // abound (32000, 4096 rows: 99.6; 100.4, 142); more while rows leave CUs free or are long: sixteen for up to 256 rows
-  // (32000: 12.0; 13.1 with eight, 17.6 with four) unless eight hold the row (12000: 7.8; 8.8 with sixteen) and for long ones
-  // (151937, 1024 rows: 120; 131, 144), eight between (32000, 512 rows: 16.7; 20.6 with four, 20.7 with sixteen).
-  if (a.vocab <= 256 * kPer)
+  // As few wavefronts a row as hold it in one tile where rows abound, since a tile costs the same half empty (2048 logits, 4096
+  // rows: 12 us with one, 26 with four), but four for few rows (2000 logits, one row, 32 alternatives: 6.8; 12.5 with one); four
+  // too where rows abound (32000, 4096 rows: 98; 100 with eight, 142 with sixteen).  More while rows leave CUs free or are
+  // long: sixteen for up to 256 rows (32000: 12.0; 13.1 with eight, 17.6 with four) unless eight hold the row (12000: 7.8; 8.8
+  // with sixteen) and for long ones (151937, 1024 rows: 120; 131, 144), eight between (32000, 512 rows: 16.7; 20.6 with
+  // four, 20.7 with sixteen).
+  if (rows > 256 && a.vocab <= 64 * kPer)
+    go(std::integral_constant<int, 64>());
+  else if (rows > 256 && a.vocab <= 128 * kPer)
+    go(std::integral_constant<int, 128>());
+  else if (a.vocab <= 256 * kPer)
     go(std::integral_constant<int, 256>());
   else if (rows <= 256 ? a.vocab > 512 * kPer : a.vocab > 65536)
     go(std::integral_constant<int, 1024>());

@@ -43,7 +43,8 @@ def check(xd, ids, k):
 @pytest.mark.parametrize("T,V,C,k", [(1, 1, 1, 1), (1, 2, 1, 2), (3, 31, 2, 31), (2, 64, 1, 32), (5, 65, 3, 5), (1, 32000, 1, 8),
                                      (7, 1023, 0, 7), (2, 50257, 4, 20), (300, 777, 1, 0), (1, 151937, 2, 32),
                                      (600, 4099, 2, 1), (33, 16384, 1, 16), (520, 9001, 1, 5), (300, 20011, 2, 32),
-                                     (260, 66001, 1, 3), (9, 8195, 1, 17)])
+                                     (260, 66001, 1, 3), (9, 8195, 1, 17), (400, 1999, 2, 32),
+                                     (257, 4095, 1, 20)])
 def test_rows(src, T, V, C, k):
     torch = torch_cuda()
     say("logprobs", src, T, V, C, k)
