@@ -1029,10 +1029,11 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   // two workgroups to a CU where there are fewer cells (30000 tokens, 64 heads over 8: 21 us; 25 with four)
   int64_t splits = (512 + p.cells - 1) / p.cells;
   if (splits < (keys + kMaxChunk - 1) / kMaxChunk) splits = (keys + kMaxChunk - 1) / kMaxChunk;
-  // Chunks of one step of the four wavefronts where the workgroup that comes last joins 3..kInline of them, else of two steps
-  // or more, since a chunk more costs more than a second step (one row of 32 heads: 200 keys 6.5 us in one chunk and 7.5 in
-  // two, 2000 keys 10.6 in eight and 11.2 in sixteen; but 511 keys 7.7 us in four and 8.5 in two).
-  const int64_t steps = ones > 2 && ones <= kInline ? 1 : 2;
+  // Up to four steps of the four wavefronts stay in one chunk, since a join costs more than two or three steps (300 keys in one chunk
+  // and in three: one row of 32 heads 7.6 us and 7.7, 4 x 16 tokens of 8 x 8 heads 8.2 and 11.2), but for four steps of few cells
+  // (511 keys of one row of 32 heads: 8.5 us in one chunk, 7.9 in four; 4 x 32 heads: 8.7, 9.3).  Longer chunks have two steps
+  // or more (2000 keys of one row of 32 heads: 10.6 us in eight chunks, 11.2 in sixteen).
+  const int64_t steps = ones <= 3 ? 3 : ones > 4 ? 2 : p.cells <= 64 ? 1 : 4;
   const int64_t most = (ones + steps - 1) / steps;
   if (splits > most) splits = most;
   if (splits > kMaxSplits) splits = kMaxSplits;
