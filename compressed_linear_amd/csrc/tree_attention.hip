@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) tree_attention_kernel(AttnArgs 
   }
 }
 
-// Many query rows of a kv head (trees of a grouped model): a workgroup has 128 rows, 32 to a wavefront, and all of them read the
+// Many query rows of a kv head and one sequence (a tree of a grouped model): a workgroup has 128 rows, 32 to a wavefront, and all of them read the
 // same keys.  Its threads widen a block of 32 keys together, K as rows of fp16 and V transposed, into one of two LDS
 // buffers while the products run on the other; so a code is widened once for 128 rows, and an operand is one 16-byte read.
 // A tree of 64 over 61441 int8 tokens, 64 query heads over 8: 191 us, 0.67 PFLOP/s.  Bound by what two wavefronts to a SIMD do
