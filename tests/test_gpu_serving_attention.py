@@ -241,6 +241,27 @@ def test_scores_and_values_of_very_different_size(kind, dtype, sharp, spread):
     say("sizes", kind, dtype, sharp, spread, p.check(p.call()))
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_past_4_gib(new):
+    torch = torch_cuda()
+    r = np.random.default_rng(23)
+    pages, page, H, D, n = 4300, 1024, 8, 128, 1500  # 4.5 GB of keys
+    cache = cla.KVCache(pages, page, H, D, "int8")
+    table = np.array([[pages - 1, pages - 30]], np.int32)
+    slots = table[0][np.arange(n) // page] * page + np.arange(n) % page
+    k, v = (torch.from_numpy(r.normal(0, 1, (n, H, D)).astype(np.float32)).cuda() for _ in range(2))
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()  # noqa: E731
+    cache.append(k, v, dev(slots))
+    ks, vs = (x.double().cpu().numpy() for x in cache.read(dev(slots), dtype=torch.float32))
+    q = torch.from_numpy(r.normal(0, 1, (new, 2 * H, D)).astype(np.float32)).cuda().half()
+    say("past 4 GiB", new)
+    got = cla.tree_attention(q, cache, dev(table), dev([n - new]), dev([0, new]), max_q=new).double().cpu().numpy()
+    see = np.concatenate([np.ones((new, n - new), bool), np.tril(np.ones((new, new), bool))], 1)
+    for h in range(2 * H):
+        want, absv, mag = ref.attention(q[:, h].double().cpu().numpy(), ks[:, h // 2], vs[:, h // 2], see, 1 / np.sqrt(D))
+        assert (np.abs(got[:, h] - want) <= ref.attention_tolerance(want, absv, mag, n, D, "f16")).all(), h
+
+
 def test_scale_argument_and_strided_queries():
     for scale in (0.0, -0.05, 1.0):
         p = Problem([130], [6], 4, 2, 64, 16, "int8", "f16", seed=2, scale=scale)
