@@ -200,7 +200,12 @@ __device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ 
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[i * V + e] = j + e >= 0 && j + e < n ? Elem<DT>::up(x[j + e]) : -INFINITY;
+        for (int e = 0; e < V; ++e) v[i * V + e] = -INFINITY;
+        if (j < n) {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (j + e >= 0 && j + e < n) v[i * V + e] = Elem<DT>::up(x[j + e]);
+        }
       }
     }
     constexpr int kGroup = 4, kGroups = kPer / kGroup;
@@ -218,10 +223,14 @@ __device__ __forceinline__ void scan(const typename Elem<DT>::raw* __restrict__ 
     const float ref = m == -INFINITY ? 0.f : m;
     float l = 0.f, w = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float d = v[i] - ref, e = __builtin_amdgcn_exp2f(d * kLog2e);
-      l += e;
-      w += fmaxf(d, -1000.f) * e;  // -inf adds nothing
+    for (int p = 0; p < 4; ++p) {
+      if (t0 + p * (kTile / 4) >= n) break;  // the rest of a row's last tile is empty
+#pragma unroll
+      for (int i = p * (kPer / 4); i < (p + 1) * (kPer / 4); ++i) {
+        const float d = v[i] - ref, e = __builtin_amdgcn_exp2f(d * kLog2e);
+        l += e;
+        w += fmaxf(d, -1000.f) * e;  // -inf adds nothing
+      }
     }
     st.l += l;
     st.w += w;

@@ -81,8 +81,8 @@ def stored(q, s, kind):
 # ---------------------------------------------------------------- attention
 def attention(q, k, v, see, scale):
     """q [t, D], k and v [n, D] float64, see [t, n] -> (o, sum_j p_j |v_j|, largest sum_i |q_i k_i| scale) per row.
-    The second carries 2^-24 of what a probability below fp16's normal range may be off, divided by that 2^-11 with which
-    attention_tolerance weighs it: such a one is kept to 2^-35 of the largest, beside V's scales that differ."""
+    The second has one term more, for probabilities below fp16's normal range, which are kept to 2^-35 of the largest:
+    2^-24 of the largest times sum_j |v_j|, as attention_tolerance weighs it with 2^-11."""
     s = (q @ k.T) * scale
     s = np.where(see, s, -np.inf)
     m = s.max(-1, keepdims=True, initial=-np.inf)
