@@ -17,7 +17,7 @@
 //
 // Bound by the read of the logits where there are rows for the whole card (4096 rows of
 // 32000 fp32 logits with 4 given tokens and 5 alternatives: 94 us, 5.6 TB/s); a single
-// row by the latency of loads, votes and joins (32000 logits, 8 alternatives: 6.9 us, without alternatives 4.9; spread
+// row by the latency of loads, votes and joins (32000 logits, 8 alternatives: 6.4 us, without alternatives 4.9; spread
 // over eight workgroups that meet at a counter it took a microsecond more).
 #include <type_traits>
 
