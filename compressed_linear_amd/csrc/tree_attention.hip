@@ -20,7 +20,12 @@
 // probabilities (V); int4 codes times their 8-bit scales are fp16 values.  Q is
 // scaled per row by a power of two into fp16's range.  So the only rounding
 // below fp32 is that of the probabilities to fp16: they are kept near 2^11 of
-// fp16's range relative to the running maximum and the largest V scale.
+// fp16's range relative to the running maximum and the largest V scale that the row has seen.
+//
+// What a row does not see must not reach it, whatever lies in memory there (a drafted token that was never stored, page 0
+// in place of a bad one): its score becomes -inf and its probability 0, and the scale of a key that no row of the
+// wavefront sees becomes 0 before it meets that 0, since 0 times an infinity or NaN is NaN.  Only blocks
+// that reach past the older tokens, or have a tile without a page, pay for it.
 //
 // The running maximum moves only when a score passes it by 2^4 (one vote of the
 // wavefront a step), so that the output is rarely rescaled.
@@ -134,6 +139,15 @@ __device__ __forceinline__ float row_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// Bits that any of 16 lanes side by side (a tile's rows) has.
+__device__ __forceinline__ uint32_t any_of_rows(uint32_t v) {
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);   // quad_perm [1, 0, 3, 2]
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);   // quad_perm [2, 3, 0, 1]
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);  // mirrored in 8
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false);  // mirrored in 16
+  return v;
+}
+
 // Two bytes code + 128, as fp16 subnormals in the halves of a word -> code * 2^-9, exactly.
 __device__ __forceinline__ uint32_t widen8(uint32_t pair) {
   const h2 a = __builtin_bit_cast(h2, pair);
@@ -157,6 +171,12 @@ __device__ __forceinline__ uint32_t widen4(uint32_t word, uint32_t word8, int i,
   return __builtin_bit_cast(uint32_t, c * s);
 }
 
+// Two fp16 values, an infinity or NaN replaced by fp16's largest.
+__device__ __forceinline__ uint32_t finite(uint32_t pair) {
+  const h2 most = {(_Float16)65504.f, (_Float16)65504.f};
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_elementwise_min(__builtin_bit_cast(h2, pair), most), -most));
+}
+
 // The scales of a block of 32 keys, two tiles of 16, that a lane needs.
 template <int KIND>
 struct Scales;
@@ -178,7 +198,7 @@ struct Rows {
   float m[RT];            // it less log2(2^kProbBits / vref): sum and the outputs carry that factor, which the quotient loses
   float sum[RT];
   int tok[RT];            // its new token
-  float vref;             // a power of two above every V scale seen (int4, where V carries its scales: 1)
+  float vref[RT];         // a power of two above every V scale that the row has seen (int8; int4's V carries its scales)
 };
 
 // The first RT x 16 rows from `row0` of Q, raw.
@@ -235,17 +255,18 @@ __device__ __forceinline__ void convert_q(const AttnArgs& a, const u4 (&raw)[RT]
     // above zero, so that a masked score of -inf stays what it is
     rows.rowc[r] = fmaxf(ldexpf(fabsf(a.scale) * 1.44269504f, e - 14 + (KIND == CL_KV_INT8 ? 9 : 0)), 1e-38f);
     rows.top[r] = rows.m[r] = kNone;
-    rows.sum[r] = 0.f;
+    rows.sum[r] = rows.vref[r] = 0.f;
   }
-  rows.vref = KIND == CL_KV_INT8 ? 0.f : 1.f;
 }
 
 // Scores of a block of 32 keys from its products: K's scales (int8), and for a block that some rows do not see whole the
 // masks.  s[r][t][i]: row l % 16 of tile r, key 16 t + 4 (l / 16) + i; j0: the block's first key; left: keys of it that exist;
-// bad: tiles without a page.  ks, vs: the scales of those keys (int8).
+// bad: tiles without a page.  ks, vs: the scales of those keys (int8); vtop: the largest vs that each row sees, of the lane's keys.
+// Returns the block's keys that have a page and that some row of the wavefront sees; vs is 0 for the others.
 template <int KIND, int RT>
-__device__ __forceinline__ void finish_scores(const AttnArgs& a, const Range& range, const Rows<RT>& rows, const float (&ks)[8],
-                                              uint32_t j0, int left, int bad, bool special, f4 (&s)[RT][2], float (&vs)[8]) {
+__device__ __forceinline__ uint32_t finish_scores(const AttnArgs& a, const Range& range, const Rows<RT>& rows, const float (&ks)[8],
+                                                  uint32_t j0, int left, int bad, bool special, f4 (&s)[RT][2], float (&vs)[8],
+                                                  float (&vtop)[RT]) {
   const int g = (threadIdx.x & 63) >> 4;
   if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
@@ -253,12 +274,15 @@ __device__ __forceinline__ void finish_scores(const AttnArgs& a, const Range& ra
 #pragma unroll
       for (int r = 0; r < RT; ++r) s[r][j / 4][j % 4] *= ks[j];
   }
-  if (!special) return;
   if constexpr (KIND == CL_KV_INT8) {
+    float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (16 * (j / 4) + 4 * g + j % 4 >= left) vs[j] = 0.f;  // no token there: the scale may be anything
+    for (int j = 0; j < 8; j += 2) top = max3(top, vs[j], vs[j + 1]);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) vtop[r] = top;
   }
+  if (!special) return ~0u;
+  uint32_t seen[RT], any = 0;
   const int64_t rel = (int64_t)j0 - range.ctx;  // place of the block's first key among the new tokens
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -280,6 +304,9 @@ __device__ __forceinline__ void finish_scores(const AttnArgs& a, const Range& ra
       }
     }
     if (left < 32) see &= (1u << left) - 1u;
+    if (rows.tok[r] >= range.n_new) see = 0;  // no such row
+    seen[r] = see;
+    any |= see;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int key = 16 * (j / 4) + 4 * g + j % 4;
@@ -289,13 +316,27 @@ __device__ __forceinline__ void finish_scores(const AttnArgs& a, const Range& ra
         s[r][j / 4][j % 4] = __builtin_nanf("");
     }
   }
+  any = any_of_rows(any) & ~((bad & 1 ? 0x0000FFFFu : 0u) | (bad & 2 ? 0xFFFF0000u : 0u));
+  if constexpr (KIND == CL_KV_INT8) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) vtop[r] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int key = 16 * (j / 4) + 4 * g + j % 4;
+      if (!((any >> key) & 1)) vs[j] = 0.f;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        if ((seen[r] >> key) & 1) vtop[r] = fmaxf(vtop[r], vs[j]);
+    }
+  }
+  return any;
 }
 
 // Probabilities of a block from its scores, as the operand of the second product; moves the running maximum, and with it
 // sums and outputs, where a score passes it by more than the slack.
 template <int KIND, int RT, int CB>
-__device__ __forceinline__ void probabilities(const f4 (&s)[RT][2], const float (&vs)[8], Rows<RT>& rows, f4 (&o)[RT][CB],
-                                              uint32_t (&p)[RT][4]) {
+__device__ __forceinline__ void probabilities(const f4 (&s)[RT][2], const float (&vs)[8], const float (&vtop)[RT], Rows<RT>& rows,
+                                              f4 (&o)[RT][CB], uint32_t (&p)[RT][4]) {
   float up[RT];
   bool move = false;
 #pragma unroll
@@ -304,23 +345,18 @@ __device__ __forceinline__ void probabilities(const f4 (&s)[RT][2], const float 
                          max3(s[r][1][2], s[r][1][3], s[r][1][3]));
     up[r] = t * rows.rowc[r];
     move |= up[r] > rows.top[r] + kSlack;
-  }
-  float vtop = 0.f;
-  if constexpr (KIND == CL_KV_INT8) {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) vtop = max3(vtop, vs[j], vs[j + 1]);
-    move |= vtop > rows.vref;
+    if constexpr (KIND == CL_KV_INT8) move |= vtop[r] > rows.vref[r];
   }
   if (__any(move)) {
-    float to = rows.vref;
-    if constexpr (KIND == CL_KV_INT8) {
-      vtop = row_max(vtop);
-      if (vtop > to) to = 2.f * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, vtop) & 0x7F800000u);
-    }
-    const float lift = to > 0.f ? __builtin_amdgcn_logf(to) - kProbBits : 0.f;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       // only a row that passed it, so that no row's roundings depend on another's
+      float lift = -kProbBits;
+      if constexpr (KIND == CL_KV_INT8) {
+        const float v = row_max(vtop[r]);
+        if (v > rows.vref[r]) rows.vref[r] = 2.f * __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0x7F800000u);
+        lift = rows.vref[r] > 0.f ? __builtin_amdgcn_logf(rows.vref[r]) - kProbBits : 0.f;
+      }
       const float high = row_max(up[r]);
       if (high > rows.top[r] + kSlack) rows.top[r] = high;
       const float next = rows.top[r] + lift, old = __builtin_amdgcn_exp2f(rows.m[r] - next);
@@ -329,7 +365,6 @@ __device__ __forceinline__ void probabilities(const f4 (&s)[RT][2], const float 
 #pragma unroll
       for (int cb = 0; cb < CB; ++cb) o[r][cb] *= old;
     }
-    rows.vref = to;
   }
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -569,7 +604,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) tree_attention_kernel(AttnArgs 
         for (int r = 0; r < RT; ++r) s[r][t] = mfma16(k, q[r][st], s[r][t]);
       }
     }
-    float ks[8], vs[8];
+    float ks[8], vs[8], vtop[RT];
     uint32_t p[RT][4];
     if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
@@ -578,8 +613,8 @@ __global__ void __launch_bounds__(64 * WAVES, 2) tree_attention_kernel(AttnArgs 
         vs[j] = Elem<CL_F16>::up((uint16_t)(sc.v[j / 4][j % 4 / 2] >> (16 * (j % 2))));
       }
     }
-    finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs);
-    probabilities<KIND>(s, vs, st, o, p);
+    const uint32_t seen = finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs, vtop);
+    probabilities<KIND>(s, vs, vtop, st, o, p);
     // ---- output
     if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
@@ -596,11 +631,11 @@ __global__ void __launch_bounds__(64 * WAVES, 2) tree_attention_kernel(AttnArgs 
       uint32_t vsc[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) vsc[j] = sc.v[j];
-      if (special) {  // where there is no token the scale may be anything
+      if (special) {  // where no row sees a token the scale may be anything
         asm volatile("");  // a branch, not eight selects a block
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (16 * (j / 4) + 4 * g + j % 4 >= left) vsc[j] = 0;
+          if (!((seen >> (16 * (j / 4) + 4 * g + j % 4)) & 1)) vsc[j] = 0;
       }
       uint32_t lo[4], hi[4];  // channels 0..3 and 4..7 of two keys, one in each half
 #pragma unroll
@@ -816,7 +851,6 @@ __global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a)
   constexpr int PIECES = D / 8;
   const auto widen = [&](const Raw& x, int i) {
     uint8_t* const to = s_mem[i & 1];
-    const int left = (int)min(n - (k0 + (uint32_t)i * kBlock), (uint32_t)kBlock);
     if (tid == 0) s_bad[i & 1] = x.bad;
     if (KIND == CL_KV_INT8 && wave == 0) (&s_scale[i & 1][0][0])[l] = Elem<CL_F16>::up(x.ks);
     u4 piece[D / 64];
@@ -846,16 +880,25 @@ __global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a)
       uint32_t w[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // no token there: the scale may be anything
-        const uint32_t s0 = vkey + 2 * j < left ? x.vs[2 * j] : 0, s1 = vkey + 2 * j + 1 < left ? x.vs[2 * j + 1] : 0;
-        mul[j] = __builtin_bit_cast(h2, s0 | s1 << 16);
+        mul[j] = __builtin_bit_cast(h2, (uint32_t)x.vs[2 * j] | (uint32_t)x.vs[2 * j + 1] << 16);
         w[j] = x.v[2 * j] | x.v[2 * j + 1] << 16;
       }
+      u2 val[VC];
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
         const int own = (c + turn) & (VC - 1);
-        *reinterpret_cast<u2*>(vt + (vch + own) * VS) = u2{widen4(w[0] >> 4 * own, 0, 0, mul[0]), widen4(w[1] >> 4 * own, 0, 0, mul[1])};
+        val[c] = u2{widen4(w[0] >> 4 * own, 0, 0, mul[0]), widen4(w[1] >> 4 * own, 0, 0, mul[1])};
       }
+      // Which keys of the block no row sees is not known yet.  There anything may come out, so it is made finite (the
+      // probabilities there are 0); a stored value is and stays as it is.
+      if (k0 + (uint32_t)(i + 1) * kBlock > (uint32_t)range.ctx || x.bad) {
+        asm volatile("");  // a branch
+#pragma unroll
+        for (int c = 0; c < VC; ++c) val[c] = u2{finite(val[c].x), finite(val[c].y)};
+      }
+#pragma unroll
+      for (int c = 0; c < VC; ++c)
+        *reinterpret_cast<u2*>(vt + (vch + ((c + turn) & (VC - 1))) * VS) = val[c];
     }
   };
   Raw x;
@@ -895,7 +938,7 @@ __global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a)
 #pragma unroll
         for (int r = 0; r < RT; ++r) s[r][t] = mfma16(kk, q[r][k], s[r][t]);
       }
-    float ks[8], vs[8];
+    float ks[8], vs[8], vtop[RT];
     if constexpr (KIND == CL_KV_INT8) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -909,8 +952,8 @@ __global__ void __launch_bounds__(256, 2) tree_attention_wide_kernel(AttnArgs a)
 #pragma unroll
     for (int cb = 0; cb < CB - 2; ++cb) vf[cb] = *reinterpret_cast<const u4*>(vt + (16 * cb + c16) * VS + 16 * g);
     uint32_t p[RT][4];
-    finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs);
-    probabilities<KIND>(s, vs, st, o, p);
+    finish_scores<KIND>(a, range, st, ks, j0, left, bad, special, s, vs, vtop);
+    probabilities<KIND>(s, vs, vtop, st, o, p);
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
       const u4 w = cb < CB - 2 ? vf[cb < CB - 2 ? cb : 0] : *reinterpret_cast<const u4*>(vt + (16 * cb + c16) * VS + 16 * g);

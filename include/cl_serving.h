@@ -140,9 +140,11 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  *                    use; calls leave them zeroed.  One call at a time may use it.
  * Scores, maxima, sums and outputs are held in fp32; keys and values enter the matrix cores exactly.  The
  * probabilities (int8: times V's scale) enter them as fp16, scaled so that those down to 2^-24 of the largest
- * (int8: of the largest probability times the largest V scale read so far, that of a masked token too) keep fp16's
+ * (int8: of the largest probability times the largest V scale that the row has seen so far) keep fp16's
  * 11 bits; below 2^-35 of it they are lost.
  * A page of block_table outside the cache, or a place past its width, gives NaN in the rows that see it.
+ * Tokens that a row does not see do not change its bits, whatever their codes and scales are in memory, if no row
+ * of the call sees them or their scales are finite: a drafted token may have been stored nowhere (slot -1).
  * Sequences whose cu_q does not fit [0, tokens] or max_q are left out (their rows are not written).
  * Deterministic: the same inputs give bitwise identical o.
  * Errors: CL_EINVAL, CL_EUNSUPPORTED (dim, max_q > 256), CL_ESIZE, CL_ENOMEM (work_bytes too small), CL_EHIP.
