@@ -52,13 +52,13 @@ _pack_rope, _pack_append, _pack_read, _pack_attention, _pack_logprobs = (
 
 _torch = None
 _lib = None
-_empty = _current_device = _raw_stream = _i32 = None
+_empty = _current_device = _raw_stream = _capturing = _i32 = None
 _DT: dict = {}
 
 
 def _setup():
     """torch and the library, loaded at the first call (importing the package needs neither)."""
-    global _torch, _lib, _empty, _current_device, _raw_stream, _i32
+    global _torch, _lib, _empty, _current_device, _raw_stream, _capturing, _i32
     if _lib is None:
         import torch
 
@@ -69,6 +69,7 @@ def _setup():
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
         _DT.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
         _lib = lib()
     return _lib
@@ -162,8 +163,8 @@ class KVCache:
     Either sizes are given and the cache allocates its tensors, or the four tensors are:
     k, v uint8 [pages, heads, page_size, dim or dim / 2]; k_scale, v_scale float16 [pages, heads,
     page_size] or [pages, heads, page_size, dim / 32].  It also keeps a workspace of `tree_attention` for
-    each stream it is called on, which a call that is recorded there shares (replays and calls on that stream take
-    turns); one that is recorded where none was called before has a workspace of the recording.
+    each stream it is called on, and one for each recording (into a graph) that it is called in: a replay may
+    run on any stream, next to other calls.
     """
 
     def __init__(self, pages: int = 0, page_size: int = 64, heads: int = 1, dim: int = 128, kind: str = "int8",
@@ -241,12 +242,15 @@ class KVCache:
             _check(st, "cl_kv_read")
         return k, v
 
-    def _workspace(self, sizes, stream):
-        """Address and bytes of a workspace for these sizes on `stream`.  In a recording it is one of the recording,
-        since what clears it runs with the replays."""
+    def _recording(self, stream):
+        """Whose workspace a call that is recorded on `stream` takes.  It is the recording's even where the stream has
+        one, with which nothing orders the replays; what clears it runs with them."""
         recording = ctypes.c_uint64()
         _check(_lib.cl_recording(stream, ctypes.byref(recording)), "cl_recording")
-        key = (stream, recording.value) if recording.value else stream
+        return stream, recording.value
+
+    def _workspace(self, sizes, key):
+        """Address and bytes of a workspace for these sizes, of a stream or of a recording on it."""
         need = _lib.cl_tree_attention_work_bytes(*sizes)
         if self._work.get(key, (0, 0))[1] < need:
             work = _empty(2 * need, dtype=_torch.uint8, device=self.device)
@@ -299,9 +303,10 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
             _index(ctx_lens, B, dev, "ctx_lens"), _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
             1.0 / D ** 0.5 if scale is None else scale, out.data_ptr())
     stream = _stream(dev)
-    st = L.cl_call(_ATTENTION, _pack_attention(*args, *cache._work.get(stream, (0, 0)), stream))
+    key = cache._recording(stream) if _capturing() else stream
+    st = L.cl_call(_ATTENTION, _pack_attention(*args, *cache._work.get(key, (0, 0)), stream))
     if st == -3:  # the workspace is too small for these sizes: make a larger one, once
-        work = cache._workspace((B, H, cache.heads, D, max_q, max_ctx), stream)
+        work = cache._workspace((B, H, cache.heads, D, max_q, max_ctx), key)
         st = L.cl_call(_ATTENTION, _pack_attention(*args, *work, stream))
     if st:
         _check(st, "cl_tree_attention")

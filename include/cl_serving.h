@@ -161,7 +161,7 @@ cl_status cl_tree_attention(const void* q, int32_t dtype, int64_t q_token, int64
 /*
  * cl_recording -- the number of the graph recording that `stream` is part of (HIP gives each its own), 0
  * if it is not recorded.  For callers that keep a workspace to a recording: what clears it runs with the
- * replays.
+ * replays, which may run on any stream next to other calls.
  * Errors: CL_EINVAL (id NULL), CL_EHIP.
  */
 cl_status cl_recording(void* stream, uint64_t* id);

@@ -1,0 +1,49 @@
+"""Workspaces of the attention: one to a stream, one to a recording (needs an MI355X)."""
+import pytest
+
+import compressed_linear_amd as cla
+from test_gpu_serving_attention import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+def test_warm_up_and_two_graphs_on_one_stream():
+    # the usual recipe: an eager call on a side stream, recordings there, replays on the main stream.  By the addresses, no two
+    # share a workspace, so nothing has to order them; every run here ends before the next begins.
+    p = Problem([400, 33, 1200], [4, 1, 7], 8, 2, 128, 32, "int8", "bf16", seed=19)
+    torch = p.torch
+    want = p.call()
+    tab, ctx, cu = p.dev(p.table), p.dev(p.ctx), p.dev(p.cu)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def call(out=None):
+        return cla.tree_attention(p.q, p.cache, tab, ctx, cu, max_q=p.max_q, max_ctx=1200, tree_mask=p.mask, out=out)
+
+    with torch.cuda.stream(s):
+        warm = call()
+    s.synchronize()
+    assert torch.equal(warm, want)
+    eager = {a for a, _ in p.cache._work.values()}
+    assert len(eager) == 2  # the main stream's and this one's
+    graphs = []
+    for _ in range(2):
+        out = torch.empty_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call(out)
+            call(out)
+        graphs.append((g, out))
+    recorded = {a for a, _ in p.cache._work.values()} - eager
+    assert len(recorded) == 2
+    for _ in range(3):
+        for g, out in graphs:
+            out.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+        with torch.cuda.stream(s):
+            again = call()
+        torch.cuda.synchronize()
+        assert torch.equal(again, want) and torch.equal(call(), want)
