@@ -69,6 +69,10 @@ constexpr int kInline = 4;
 constexpr int kFewKeys = 256;      // up to which many cells are a wavefront each
 constexpr int kMaxCells = 65536;   // cells (sequence, kv head, row group) that may be joined so: their counters open the workspace
 constexpr int kMaxSplits = 1024;   // chunks that a sequence's keys are cut into
+// Bytes of partial outputs: past them the cells alone fill the card many times over, and longer chunks cost nothing (64 x 64 tokens of
+// 64 heads over 8, one sequence of 131072 among short ones: 1.32 ms, 1.49 with the 4.3 GB that chunks of kMaxChunk want, 1.39
+// with 1 GiB; 64 x 16 tokens 425 us, 434 with 1.1 GB, 475 with 256 MiB; 256 single tokens 514, 501 with 537 MB).
+constexpr int64_t kMaxParts = (int64_t)512 << 20;
 
 constexpr size_t kCounterBytes = kMaxCells * sizeof(uint32_t);
 static_assert(kCounterBytes == CL_ATTENTION_COUNTER_BYTES, "the header's figure");
@@ -1080,6 +1084,8 @@ AttnPlan plan_attention(int64_t sequences, int q_heads, int heads, int dim, int 
   const int64_t most = (ones + steps - 1) / steps;
   if (splits > most) splits = most;
   if (splits > kMaxSplits) splits = kMaxSplits;
+  const int64_t fit = kMaxParts / (p.cells * p.group_rows * (int64_t)(dim * sizeof(float) + sizeof(float2)));
+  if (splits > fit) splits = fit > 1 ? fit : 1;
   p.chunk = (int)((((keys + splits - 1) / splits) + unit - 1) / unit * unit);
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
   // One wavefront where a cell is one block of keys, or where few keys meet more cells than the card holds workgroups of four:

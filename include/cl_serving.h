@@ -136,8 +136,9 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  *                    are ignored.
  *   scale            of the scores, finite
  *   work             device, cl_tree_attention_work_bytes(...) bytes for these arguments, 16-byte aligned (may be
- *                    NULL where that is 0).  Its first CL_ATTENTION_COUNTER_BYTES are zeroed once before its first
- *                    use; calls leave them zeroed.  One call at a time may use it.
+ *                    NULL where that is 0; never more than CL_ATTENTION_COUNTER_BYTES + 2^29).  Its first
+ *                    CL_ATTENTION_COUNTER_BYTES are zeroed once before its first use; calls leave them zeroed.  One
+ *                    call at a time may use it.
  * Scores, maxima, sums and outputs are held in fp32; keys and values enter the matrix cores exactly.  The
  * probabilities (int8: times V's scale) enter them as fp16, scaled so that those down to 2^-24 of the largest
  * (int8: of the largest probability times the largest V scale that the row has seen so far) keep fp16's

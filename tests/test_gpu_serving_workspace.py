@@ -47,3 +47,12 @@ def test_warm_up_and_two_graphs_on_one_stream():
             again = call()
         torch.cuda.synchronize()
         assert torch.equal(again, want) and torch.equal(call(), want)
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+@pytest.mark.parametrize("new,hint", [(64, 131072), (2, 2 ** 31 - 1), (33, 1000000)])
+def test_chunks_that_the_workspace_limits(kind, new, hint):
+    # many rows and a hint far past the real lengths: longer, fewer chunks, or one
+    p = Problem([9000] + [20 * i for i in range(39)], [new] * 40, 16, 8, 64, 64, kind, "bf16", mask="tree", seed=61)
+    p.check(p.call(max_ctx=hint))
+    assert p.torch.equal(p.call(max_ctx=hint), p.call(max_ctx=hint))

@@ -76,3 +76,16 @@ def test_counters_are_cleared_where_a_workspace_is_made(stand):
         stand.call(stream, recording)
     assert len({work for _, work, _ in stand.lib.calls}) == 3
     assert all(not any(ctypes.string_at(work, serving.COUNTER_BYTES)) for _, work, _ in stand.lib.calls)
+
+
+def test_workspace_stays_bounded():
+    # the longest contexts on many sequences with many rows, as a wide block table asks for
+    need = cla.lib().cl_tree_attention_work_bytes
+    for B in (1, 3, 64, 1000, 65535):
+        for hq, hkv in ((1, 1), (64, 8), (64, 64), (8, 1)):
+            for dim in (64, 128):
+                for T in (1, 16, 64, 256):
+                    for ctx in (0, 5000, 131072, 2 ** 31 - 1):
+                        assert 0 <= need(B, hq, hkv, dim, T, ctx) <= serving.COUNTER_BYTES + 2 ** 29, (B, hq, hkv, dim, T, ctx)
+    # ordinary sizes still cut their keys
+    assert need(1, 64, 8, 128, 1, 131001) > 0 and need(64, 64, 8, 128, 16, 8000) > 0
