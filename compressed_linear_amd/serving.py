@@ -18,6 +18,8 @@ ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 KV_KIND = {"int8": 0, "int4": 1}
 COUNTER_BYTES = 262144  # CL_ATTENTION_COUNTER_BYTES
+_ROOM = 32 << 20        # bytes that a workspace may have beyond what its call needs
+_ENDED = 4              # recordings that a cache may list before it asks which have ended
 
 
 class cl_kv_cache(ctypes.Structure):
@@ -163,8 +165,8 @@ class KVCache:
     Either sizes are given and the cache allocates its tensors, or the four tensors are:
     k, v uint8 [pages, heads, page_size, dim or dim / 2]; k_scale, v_scale float16 [pages, heads,
     page_size] or [pages, heads, page_size, dim / 32].  It also keeps a workspace of `tree_attention` for
-    each stream it is called on, and one for each recording (into a graph) that it is called in: a replay may
-    run on any stream, next to other calls.
+    each stream it is called on, and one for each recording (torch.cuda.graph) that it is called in: a replay may
+    run on any stream, next to other calls.  A recording's lies in its graph's own memory, and goes with it.
     """
 
     def __init__(self, pages: int = 0, page_size: int = 64, heads: int = 1, dim: int = 128, kind: str = "int8",
@@ -201,7 +203,8 @@ class KVCache:
                                  heads, dim, KV_KIND[kind], 0)
         self._ref = ctypes.addressof(self._desc)
         self._work: dict = {}   # by stream, or stream and recording: address and bytes of the workspace
-        self._keep: list = []   # their tensors, outgrown ones too: a recorded graph may still use them
+        self._keep: dict = {}   # their tensors
+        self._recorded = 0      # how many of them are recordings'
 
     def append(self, k, v, slots, positions=None, table=None, layout: str = "half"):
         """Quantise new keys and values [tokens, heads, dim] into `slots` (int32 [tokens]; a slot outside the
@@ -249,14 +252,27 @@ class KVCache:
         _check(_lib.cl_recording(stream, ctypes.byref(recording)), "cl_recording")
         return stream, recording.value
 
+    def _let_go(self):
+        """Drops the workspaces of recordings that have ended.  torch allocated them from their graph's memory, which
+        stays the graph's until it is deleted."""
+        now = ctypes.c_uint64()
+        for key in [k for k in self._work if type(k) is tuple]:
+            if _lib.cl_recording(key[0], ctypes.byref(now)) or now.value != key[1]:
+                del self._work[key], self._keep[key]
+                self._recorded -= 1
+
     def _workspace(self, sizes, key):
-        """Address and bytes of a workspace for these sizes, of a stream or of a recording on it."""
+        """Address and bytes of a workspace for these sizes, of a stream or of a recording on it.  An outgrown one can
+        go at once: its memory is given out again on its stream only, after the calls that use it."""
+        if self._recorded >= _ENDED and key not in self._work:
+            self._let_go()
         need = _lib.cl_tree_attention_work_bytes(*sizes)
-        if self._work.get(key, (0, 0))[1] < need:
-            work = _empty(2 * need, dtype=_torch.uint8, device=self.device)
-            work[:COUNTER_BYTES].zero_()  # the calls leave them so
-            self._keep.append(work)
-            self._work[key] = work.data_ptr(), 2 * need
+        size = need + min(need, _ROOM)
+        work = self._keep[key] = _empty(size, dtype=_torch.uint8, device=self.device)
+        work[:COUNTER_BYTES].zero_()  # the calls leave them so
+        if type(key) is tuple and key not in self._work:
+            self._recorded += 1
+        self._work[key] = work.data_ptr(), size
         return self._work[key]
 
 
@@ -303,7 +319,12 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
             _index(ctx_lens, B, dev, "ctx_lens"), _index(cu_q, B + 1, dev, "cu_q"), max_q, max_ctx, mp, words,
             1.0 / D ** 0.5 if scale is None else scale, out.data_ptr())
     stream = _stream(dev)
-    key = cache._recording(stream) if _capturing() else stream
+    if _capturing():
+        key = cache._recording(stream)
+    else:
+        key = stream
+        if cache._recorded:
+            cache._let_go()
     st = L.cl_call(_ATTENTION, _pack_attention(*args, *cache._work.get(key, (0, 0)), stream))
     if st == -3:  # the workspace is too small for these sizes: make a larger one, once
         work = cache._workspace((B, H, cache.heads, D, max_q, max_ctx), key)

@@ -1,6 +1,8 @@
 """Which workspace a call of the attention gets: by stream and by recording (no GPU: the library is stood in for)."""
 import ctypes
+import gc
 import struct
+import weakref
 
 import pytest
 
@@ -89,3 +91,53 @@ def test_workspace_stays_bounded():
                         assert 0 <= need(B, hq, hkv, dim, T, ctx) <= serving.COUNTER_BYTES + 2 ** 29, (B, hq, hkv, dim, T, ctx)
     # ordinary sizes still cut their keys
     assert need(1, 64, 8, 128, 1, 131001) > 0 and need(64, 64, 8, 128, 16, 8000) > 0
+
+
+class Alive:
+    """Counts the workspaces that are still held."""
+
+    def __init__(self, monkeypatch):
+        self.refs, empty = [], serving._empty
+
+        def noted(*a, **kw):
+            t = empty(*a, **kw)
+            if t.dtype == torch.uint8:
+                self.refs.append(weakref.ref(t))
+            return t
+        monkeypatch.setattr(serving, "_empty", noted)
+
+    def sizes(self):
+        gc.collect()
+        return [r().numel() for r in self.refs if r() is not None]
+
+
+def test_outgrown_workspaces_are_returned(stand, monkeypatch):
+    alive = Alive(monkeypatch)
+    for need in (1 << 20, 5 << 20, 30 << 20, 100 << 20):
+        stand.lib.need = need
+        stand.call(1)
+        (size,) = alive.sizes()
+        assert need <= size <= need + (32 << 20)  # room to grow, but not another hundred megabytes
+    stand.lib.need = 1 << 20
+    stand.call(1)
+    assert len(alive.refs) == 4
+
+
+def test_recordings_that_ended_hold_no_workspace(stand, monkeypatch):
+    # a graph's memory is its own: once it is recorded, the cache lets its workspace go
+    alive = Alive(monkeypatch)
+    stand.call(1)
+    for i in range(1, 4):
+        stand.call(2, recording=i)
+        stand.call(2, recording=i)
+    stand.call(3, recording=9)  # still under way below
+    stand.lib.recording[2] = 0
+    mine = stand.call(3, recording=9)
+    stand.call(1)
+    assert len(alive.sizes()) == 2 and stand.call(3, recording=9) == mine
+    stand.lib.recording[3] = 0
+    stand.call(1)
+    assert len(alive.sizes()) == 1
+    for i in range(20, 60):  # recorded again and again, with no other call between
+        stand.call(2, recording=i)
+    assert len(alive.sizes()) <= 6
