@@ -295,7 +295,7 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
     qt, qh, one = q.stride()
     qp = q.data_ptr()
     if one != 1 or qt % 8 or qh % 8 or qp % 16:
-        q = q.contiguous()
+        q = q.clone(memory_format=_torch.contiguous_format)  # contiguous() leaves one that only lies at an odd address
         qt, qh, _ = q.stride()
         qp = q.data_ptr()
     T, H, D = shape
