@@ -336,7 +336,14 @@ template <int DT>
 void launch_logprobs(const LogprobArgs& a, int rows, hipStream_t s) {
   const auto go = [&](auto threads) {
     constexpr int n = decltype(threads)::value;
-    hipLaunchKernelGGL((logprobs_kernel<DT, n>), dim3(rows), dim3(n), 0, s, a);
+    in_pieces(rows, n, [&](int64_t first, int64_t count) {
+      LogprobArgs b = a;
+      b.x = beyond(a.x, DT, first * a.x_row);
+      if (a.given) b.ids += first * a.given, b.logp += first * a.given;
+      b.entropy += first;
+      if (a.top_k) b.top_ids += first * a.top_k, b.top_logp += first * a.top_k;
+      hipLaunchKernelGGL((logprobs_kernel<DT, n>), dim3((unsigned)count), dim3(n), 0, s, b);
+    });
   };
   // As few wavefronts a row as hold it in one tile where rows abound, since a tile costs the same half empty (2048 logits, 4096
   // rows: 12 us with one, 26 with four), but four for few rows (2000 logits, one row, 32 alternatives: 6.8; 12.5 with one); four

@@ -17,8 +17,8 @@ struct RopeScale {
 };
 
 __global__ void __launch_bounds__(256) rope_table_kernel(float2* __restrict__ table, int positions, int half, int rot,
-                                                         RopeScale r) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                         int64_t first, RopeScale r) {
+  const int64_t at = first * half + (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= (int64_t)positions * half) return;
   const int p = (int)(at / half), i = (int)(at % half);
   double w = pow(r.base, -2.0 * i / rot);
@@ -316,19 +316,32 @@ __global__ void __launch_bounds__(256) kv_read_kernel(cl_kv_cache c, int page_sh
 // The largest power of two (its logarithm) up to 16 that divides the heads.
 int heads_side_by_side(int heads) { return std::min(__builtin_ctz(heads), 4); }
 
+// A launch's part of a call: tokens [first, first + count).
+RopeArgs piece_of(RopeArgs a, int in, int out, int64_t first, int64_t count) {
+  a.x = beyond(a.x, in, first * a.x_token);
+  a.y = beyond(a.y, out, first * a.y_token);
+  a.positions += first;
+  a.tokens = (int)count;
+  return a;
+}
+
 template <int IN, int OUT>
 void launch_rope(const RopeArgs& a, hipStream_t s) {
   const bool vec = a.rot % 16 == 0 && a.dim % 16 == 0 && aligned_to(a.table, 16) &&
                    heads_aligned(a.x, IN, a.x_token, a.x_head) && heads_aligned(a.y, OUT, a.y_token, a.y_head);
-  const auto grid = [](int64_t n) { return dim3((unsigned)((n + 255) / 256)); };
+  const auto go = [&](auto kernel, int64_t each) {
+    in_pieces(a.tokens, each, [&](int64_t first, int64_t count) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((count * each + 255) / 256)), dim3(256), 0, s, piece_of(a, IN, OUT, first, count));
+    });
+  };
   if (!vec)
-    hipLaunchKernelGGL((rope_pair_kernel<IN, OUT>), grid((int64_t)a.tokens * a.heads * ((a.dim + 1) / 2)), dim3(256), 0, s, a);
+    go(rope_pair_kernel<IN, OUT>, (int64_t)a.heads * ((a.dim + 1) / 2));
   // Two heads to a thread for many tokens of 16 bits, whose heads are no larger than the cosines and sines (8192 x 72 heads, half
   // of each rotated: 53 us, 55.5 with one and 54 with four; fp32 83 against 81.5; 64 tokens 3.3 against 3.0).
   else if (IN != CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17))
-    hipLaunchKernelGGL((rope_kernel<IN, OUT, 2>), grid((int64_t)a.tokens * ((a.heads + 1) / 2) * (a.dim / 16)), dim3(256), 0, s, a);
+    go(rope_kernel<IN, OUT, 2>, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
   else
-    hipLaunchKernelGGL((rope_kernel<IN, OUT, 1>), grid((int64_t)a.tokens * a.heads * (a.dim / 16)), dim3(256), 0, s, a);
+    go(rope_kernel<IN, OUT, 1>, (int64_t)a.heads * (a.dim / 16));
 }
 
 template <int IN>
@@ -345,12 +358,19 @@ template <int IN, int KIND, int D>
 void launch_append(const AppendArgs& a, hipStream_t s) {
   const bool vec = heads_aligned(a.src[0], IN, a.token[0], a.head[0]) && heads_aligned(a.src[1], IN, a.token[1], a.head[1]) &&
                    a.rot % 16 == 0;
-  const int each = 256 / (D / 8) >> a.side;
-  const dim3 grid((unsigned)(((int64_t)a.tokens + each - 1) / each), a.c.heads >> a.side, 2);
-  if (vec)
-    hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, true>), grid, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, false>), grid, dim3(256), 0, s, a);
+  const int each = 256 / (D / 8) >> a.side;  // tokens of a workgroup
+  in_pieces(a.tokens, (D / 8) << a.side, [&](int64_t first, int64_t count) {
+    AppendArgs b = a;
+    for (int w = 0; w < 2; ++w) b.src[w] = beyond(a.src[w], IN, first * a.token[w]);
+    b.slots += first;
+    if (a.table) b.positions += first;
+    b.tokens = (int)count;
+    const dim3 grid((unsigned)((count + each - 1) / each), a.c.heads >> a.side, 2);
+    if (vec)
+      hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, true>), grid, dim3(256), 0, s, b);
+    else
+      hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, false>), grid, dim3(256), 0, s, b);
+  });
 }
 
 template <int IN>
@@ -372,8 +392,11 @@ template <int OUT, int KIND, int D>
 void launch_read(const cl_kv_cache& c, const int32_t* slots, int n, void* ko, void* vo, hipStream_t s) {
   typedef typename Elem<OUT>::raw raw;
   const int side = heads_side_by_side(c.heads), slots_each = 2 * 256 / (D / 8) >> side;
-  hipLaunchKernelGGL((kv_read_kernel<OUT, KIND, D>), dim3((unsigned)(((int64_t)n + slots_each - 1) / slots_each), c.heads >> side),
-                     dim3(256), 0, s, c, __builtin_ctz(c.page_size), side, slots, n, static_cast<raw*>(ko), static_cast<raw*>(vo));
+  in_pieces(n, (D / 8) << side, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL((kv_read_kernel<OUT, KIND, D>), dim3((unsigned)((count + slots_each - 1) / slots_each), c.heads >> side),
+                       dim3(256), 0, s, c, __builtin_ctz(c.page_size), side, slots + first, (int)count,
+                       static_cast<raw*>(ko) + first * c.heads * D, static_cast<raw*>(vo) + first * c.heads * D);
+  });
 }
 
 template <int OUT>
@@ -389,12 +412,6 @@ void launch_read(const cl_kv_cache& c, const int32_t* slots, int n, void* ko, vo
     else
       launch_read<OUT, CL_KV_INT4, 64>(c, slots, n, ko, vo, s);
   }
-}
-
-// Workgroups of 256 threads for n threads; 0 where the grid would be too large.
-unsigned grid_of(int64_t n) {
-  const int64_t g = (n + 255) / 256;
-  return g > 0x7FFFFFFFll ? 0u : (unsigned)g;
 }
 
 }  // namespace
@@ -432,10 +449,10 @@ extern "C" cl_status cl_rope_table(int32_t positions, int32_t rot, double base, 
     r.span = hi - lo > 0.001 ? hi - lo : 0.001;
     r.gain = 0.1 * log(factor) + 1.0;
   }
-  const unsigned grid = grid_of((int64_t)positions * (rot / 2));
-  if (!grid) return fail(CL_ESIZE, "rope table: too many positions");
-  hipLaunchKernelGGL(rope_table_kernel, dim3(grid), dim3(256), 0, static_cast<hipStream_t>(stream),
-                     reinterpret_cast<float2*>(table), positions, rot / 2, rot, r);
+  in_pieces(positions, rot / 2, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL(rope_table_kernel, dim3((unsigned)((count * (rot / 2) + 255) / 256)), dim3(256), 0,
+                       static_cast<hipStream_t>(stream), reinterpret_cast<float2*>(table), (int)(first + count), rot / 2, rot, first, r);
+  });
   return launched("rope table");
 }
 
@@ -458,7 +475,7 @@ extern "C" cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, in
   if ((int64_t)tokens * heads >= ((int64_t)1 << 40) / dim) return fail(CL_ESIZE, "rope: tokens * heads * dim at 2^40 or more");
   const RopeArgs a = {x, y, positions, reinterpret_cast<const float2*>(table), x_token, x_head, y_token, y_head,
                       tokens, heads, dim, rot, layout, table_rows};
-  if (!grid_of((int64_t)tokens * heads * ((dim + 1) / 2))) return fail(CL_ESIZE, "rope: too many tokens");
+  if ((int64_t)heads * ((dim + 1) / 2) > kLaunch) return fail(CL_ESIZE, "rope: too many heads");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (x_dtype == CL_F16)
     launch_rope<CL_F16>(y_dtype, a, s);

@@ -107,6 +107,19 @@ inline bool heads_aligned(const void* p, int dtype, int64_t token, int64_t head)
   return aligned_to(p, 16) && token * e % 16 == 0 && head * e % 16 == 0;
 }
 
+// A launch holds fewer than 2^32 threads along a dimension (the runtime drops the rest without an error), so longer work goes
+// in pieces: f(first, count) over n tokens (rows) of `each` threads in workgroups of at most 1024, where one token fits.
+constexpr int64_t kLaunch = ((int64_t)1 << 32) - 1024;
+template <typename F>
+void in_pieces(int64_t n, int64_t each, F f) {
+  const int64_t most = kLaunch / each;
+  for (int64_t at = 0; at < n; at += most) f(at, n - at < most ? n - at : most);
+}
+
+// An address `n` elements on.
+inline const void* beyond(const void* p, int dtype, int64_t n) { return static_cast<const uint8_t*>(p) + n * (int64_t)elem_size(dtype); }
+inline void* beyond(void* p, int dtype, int64_t n) { return static_cast<uint8_t*>(p) + n * (int64_t)elem_size(dtype); }
+
 inline cl_status launched(const char* what) {
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? CL_OK : fail(CL_EHIP, "%s: launch failed: %s", what, hipGetErrorString(e));

@@ -58,7 +58,7 @@ cl_status cl_rope_table(int32_t positions, int32_t rot, double base, int32_t sca
  *   y, y_dtype            device, [tokens, heads, dim], strides y_token, y_head.  y may be x (same
  *                         type and strides); otherwise the two must not overlap.
  * Errors: CL_EINVAL (sizes, rot odd or not in [2, dim], unknown type or layout, NULL pointers, an address
- * that is no multiple of its element), CL_ESIZE (dim > 1024, tokens * heads * dim >= 2^40), CL_EHIP.
+ * that is no multiple of its element), CL_ESIZE (dim > 1024, tokens * heads * dim >= 2^40, heads * dim near 2^33), CL_EHIP.
  */
 cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, int64_t x_head, int32_t tokens, int32_t heads,
                   int32_t dim, const int32_t* positions, const float* table, int32_t table_rows, int32_t rot,
