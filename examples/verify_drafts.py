@@ -75,11 +75,8 @@ class Block:
         Returns the accepted tokens' indices, the token that follows them, and each draft's log probability and the
         entropy of what it was drawn from (both after its parent)."""
         dev, T = tokens.device, len(tokens)
-        mask, depth = torch.zeros(T, dtype=torch.int64), torch.zeros(T, dtype=torch.int64)
-        for i, p in enumerate(parents):
-            mask[i] = (mask[p] if p >= 0 else 0) | (1 << i)
-            depth[i] = depth[p] + 1 if p >= 0 else 0
-        logits = self.forward(tokens, depth.to(dev), mask[:, None].to(dev))
+        mask, depth = tree_of(parents)
+        logits = self.forward(tokens, depth.to(dev), mask.to(dev))
         # what each draft says of its children (up to 4, else padding -1) and its own first choice
         children = [[j for j in range(T) if parents[j] == i][:4] for i in range(T)]
         given = torch.tensor([[int(tokens[j]) for j in c] + [-1] * (4 - len(c)) for c in children], dtype=torch.int32, device=dev)
@@ -106,6 +103,16 @@ class Block:
             for t in (self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale):
                 t[dst // PAGE, :, dst % PAGE] = t[src // PAGE, :, src % PAGE]
         self.n += len(path)
+
+
+def tree_of(parents):
+    """Each token's ancestors and itself as bits [tokens, 1], and its depth; at most 64 tokens."""
+    mask, depth = [], []
+    for i, p in enumerate(parents):
+        mask.append((mask[p] if p >= 0 else 0) | 1 << i)
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    # bit 63 is int64's sign
+    return torch.tensor([[m - (1 << 64) if m >> 63 else m] for m in mask]), torch.tensor(depth)
 
 
 def norm(h):
