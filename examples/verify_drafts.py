@@ -49,6 +49,7 @@ class Block:
     def forward(self, tokens, depth, tree_mask=None):
         """Logits of new tokens at the sequence's end; depth: each one's place after the tokens that stay."""
         T, dev = len(tokens), self.embed.device
+        room(self.n, T)
         h = self.embed[tokens]
         position = (self.n + depth).to(torch.int32)
         slot = self.slots(torch.arange(self.n, self.n + T, device=dev))
@@ -63,6 +64,8 @@ class Block:
 
     def prompt(self, tokens):
         """Takes the prompt in; returns the next token's first choices."""
+        if not len(tokens):
+            raise ValueError("an empty prompt")
         for at in range(0, len(tokens), MAX_NEW):
             part = tokens[at:at + MAX_NEW]
             logits = self.forward(part, torch.arange(len(part), device=part.device))
@@ -103,6 +106,14 @@ class Block:
             for t in (self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale):
                 t[dst // PAGE, :, dst % PAGE] = t[src // PAGE, :, src % PAGE]
         self.n += len(path)
+
+
+def room(n, new):
+    """Refuses new tokens that the layers or the sequence's pages do not hold (an index past the pages is an error on the GPU)."""
+    if not 1 <= new <= MAX_NEW:
+        raise ValueError("%d new tokens; 1 to %d at a time" % (new, MAX_NEW))
+    if n + new > PAGE * PAGES:
+        raise ValueError("%d tokens and %d new ones in pages for %d" % (n, new, PAGE * PAGES))
 
 
 def tree_of(parents):

@@ -21,3 +21,19 @@ def test_trees_of_up_to_64_drafts():
                 up.add(at)
                 at, n = parents[at], n + 1
             assert {j for j in range(64) if (int(mask[i, 0]) >> j) & 1} == up and int(depth[i]) == n
+
+
+def test_more_tokens_than_the_pages_hold_are_refused():
+    import verify_drafts as ex
+    most = ex.PAGE * ex.PAGES
+    for n, new in ((0, 1), (0, ex.MAX_NEW), (most - 5, 5)):
+        ex.room(n, new)
+    for n, new in ((most, 1), (most - 5, 6), (0, ex.MAX_NEW + 1), (3, 0)):
+        with pytest.raises(ValueError):
+            ex.room(n, new)
+    block = object.__new__(ex.Block)  # refused before anything is done
+    block.n, block.embed = most - 1, torch.zeros(2, 2)
+    with pytest.raises(ValueError, match="pages"):
+        block.forward(torch.tensor([0, 1]), torch.tensor([0, 1]))
+    with pytest.raises(ValueError, match="empty"):
+        block.prompt(torch.tensor([], dtype=torch.int64))
