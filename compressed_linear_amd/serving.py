@@ -14,7 +14,19 @@ from typing import Optional
 SERVING_SYMBOLS = ["cl_rope_table", "cl_rope", "cl_kv_append", "cl_kv_read", "cl_tree_attention_work_bytes",
                    "cl_tree_attention", "cl_recording", "cl_token_logprobs", "cl_call"]
 
-ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+
+class UnknownName(ValueError, KeyError):
+    """An argument that names none of the choices."""
+
+    __str__ = ValueError.__str__
+
+
+class _Names(dict):
+    def __missing__(self, name):
+        raise UnknownName(f"{name!r} is none of {list(self)}")
+
+
+ROPE_LAYOUT = _Names(half=0, interleaved=1)
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 KV_KIND = {"int8": 0, "int4": 1}
 COUNTER_BYTES = 262144  # CL_ATTENTION_COUNTER_BYTES
