@@ -60,10 +60,11 @@ struct Stat {
 };
 __device__ __forceinline__ void join(Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
-  // a side without a logit above -inf has l = w = 0 and adds nothing
+  // a side without a logit above -inf has l = w = 0 and adds nothing; nor does one far below, whose d times l may be past fp32 (a
+  // row masked with the type's lowest value), so d is not taken below -1000 there, where e^d is 0
   const float da = a.m == m ? 0.f : a.m - m, db = b.m == m ? 0.f : b.m - m;
   const float ea = __builtin_amdgcn_exp2f(da * kLog2e), eb = __builtin_amdgcn_exp2f(db * kLog2e);
-  a.w = ea * (a.w + (da == -INFINITY ? 0.f : da * a.l)) + eb * (b.w + (db == -INFINITY ? 0.f : db * b.l));
+  a.w = ea * (a.w + fmaxf(da, -1000.f) * a.l) + eb * (b.w + fmaxf(db, -1000.f) * b.l);
   a.l = ea * a.l + eb * b.l;
   a.m = m;
 }
