@@ -298,7 +298,9 @@ def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, m
     cache pages.  tree_mask int64 [tokens, words]: bit i of a row is set where the row's token sees
     new token i of its sequence (None: the tokens form a chain).  max_q is at least every sequence's number
     of new tokens (at most 256); max_ctx the longest context, which sizes the launch (default: what the
-    block table holds).  Returns [tokens, q_heads, dim] of q's type."""
+    block table holds).  Returns [tokens, q_heads, dim] of q's type: `out`, or a new tensor.  Rows of a sequence
+    with more than max_q new tokens, and rows past the last sequence, are not written: in a new tensor they hold
+    whatever was in memory."""
     L = _lib or _setup()
     dev = cache.device
     shape, dt = q.shape, _DT.get(q.dtype, 2)
@@ -350,7 +352,8 @@ def token_logprobs(logits, ids, top_k: int = 0):
     """Log probabilities of given tokens (cl_token_logprobs): logits [rows, vocab] float16, bfloat16 or float32,
     ids int32 [rows, given].  Returns (logp float32 [rows, given], entropy float32 [rows]) and, with top_k > 0
     (at most 32), top_ids int32 [rows, top_k] and top_logp float32 [rows, top_k]: the largest logits first,
-    equal ones by the lower id.  An id outside the vocabulary gives NaN."""
+    equal ones by the lower id.  An id outside the vocabulary gives NaN.  The outputs are parts of one allocation,
+    which lives as long as any of them."""
     L = _lib or _setup()
     shape, dt = logits.shape, _DT.get(logits.dtype)
     if len(shape) != 2 or dt is None or not logits.is_cuda:

@@ -58,7 +58,7 @@ cl_status cl_rope_table(int32_t positions, int32_t rot, double base, int32_t sca
  *   y, y_dtype            device, [tokens, heads, dim], strides y_token, y_head.  y may be x (same
  *                         type and strides); otherwise the two must not overlap.
  * Errors: CL_EINVAL (sizes, rot odd or not in [2, dim], unknown type or layout, NULL pointers, an address
- * that is no multiple of its element), CL_ESIZE (dim > 1024, tokens * heads * dim >= 2^40, heads * dim near 2^33), CL_EHIP.
+ * that is no multiple of its element), CL_ESIZE (dim > 1024, tokens * heads * dim >= 2^40, heads * dim >= 2^33), CL_EHIP.
  */
 cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, int64_t x_head, int32_t tokens, int32_t heads,
                   int32_t dim, const int32_t* positions, const float* table, int32_t table_rows, int32_t rot,
@@ -139,14 +139,16 @@ cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, 
  *                    NULL where that is 0; never more than CL_ATTENTION_COUNTER_BYTES + 2^29).  Its first
  *                    CL_ATTENTION_COUNTER_BYTES are zeroed once before its first use; calls leave them zeroed.  One
  *                    call at a time may use it.
- * Scores, maxima, sums and outputs are held in fp32; keys and values enter the matrix cores exactly.  The
+ * Scores, maxima, sums and outputs are held in fp32; keys and values enter the matrix cores exactly, and queries as fp16,
+ * each row scaled by a power of two: channels below 2^-27 of the row's largest are kept to 2^-38 of it.  The
  * probabilities (int8: times V's scale) enter them as fp16, scaled so that those down to 2^-24 of the largest
  * (int8: of the largest probability times the largest V scale that the row has seen so far) keep fp16's
  * 11 bits; below 2^-35 of it they are lost.
  * A page of block_table outside the cache, or a place past its width, gives NaN in the rows that see it.
  * Tokens that a row does not see do not change its bits, whatever their codes and scales are in memory, if no row
  * of the call sees them or their scales are finite: a drafted token may have been stored nowhere (slot -1).
- * Sequences whose cu_q does not fit [0, tokens] or max_q are left out (their rows are not written).
+ * Sequences whose cu_q does not fit [0, tokens] or max_q are left out: their rows, and those from cu_q[sequences] on, are
+ * not written.
  * Deterministic: the same inputs give bitwise identical o.
  * Errors: CL_EINVAL, CL_EUNSUPPORTED (dim, max_q > 256), CL_ESIZE, CL_ENOMEM (work_bytes too small), CL_EHIP.
  */
