@@ -70,7 +70,8 @@ def test_a_recorded_call_shares_no_workspace(stand):
     second = stand.call(1, recording=8)
     other = stand.call(2, recording=8)  # a branch of the same recording
     assert first == again and len({eager, first, second, other}) == 4
-    assert stand.call(1) == eager and stand.call(2) not in (eager, first, second, other)
+    # the recordings end: here their memory may be given out again, on the GPU it is the graphs'
+    assert stand.call(1) == eager and stand.call(2) != eager
 
 
 def test_counters_are_cleared_where_a_workspace_is_made(stand):
