@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
 
 // 16-byte pieces: a thread owns 16 channels of a head -- eight pairs, as two runs of 8 channels in either layout, or
 // 16 channels that are copied -- of HEADS heads of a token, which then load its cosines and sines (from the caches for all
-// heads but one) once.  Bound by memory, a step by the launch (72 heads of 128, fp32 to bf16: one token 2.3 us, 8192 tokens
+// heads but one) once.  Bound by memory, a step by the launch (72 heads of 128, fp32 to bf16: one token 2.4 us, 8192 tokens
 // 81 us, 5.7 TB/s).
 template <int IN, int OUT, int HEADS>
 __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {

@@ -38,7 +38,7 @@
 // Bound for single tokens by memory: 64 sequences of up to 8192 int8 tokens (64 query heads over 8) 126 us, 5.4 TB/s, where
 // the loads alone take 125 (they come as 8 KB a wavefront and step; twice that in flight gained nothing).  By the vector
 // instructions that widen int4: 131001 tokens 35 us, 4.4 TB/s.  By the latency of its chain (lengths, pages, keys,
-// join) for a short sequence: 511 tokens of 32 heads 7.3 us.  By the softmax's vector instructions and the operands' way out
+// join) for a short sequence: 511 tokens of 32 heads 7.4 us.  By the softmax's vector instructions and the operands' way out
 // of LDS for many rows (see the wide kernel).
 #include "serving.h"
 #include "unpack.h"
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(64 * WAVES, 2) tree_attention_kernel(AttnArgs 
 // Many query rows of a kv head and one sequence (a tree of a grouped model): a workgroup has 128 rows, 32 to a wavefront, and all of them read the
 // same keys.  Its threads widen a block of 32 keys together, K as rows of fp16 and V transposed, into one of two LDS
 // buffers while the products run on the other; so a code is widened once for 128 rows, and an operand is one 16-byte read.
-// A tree of 64 over 61441 int8 tokens, 64 query heads over 8: 191 us, 0.67 PFLOP/s.  Bound by what two wavefronts to a SIMD do
+// A tree of 64 over 61441 int8 tokens, 64 query heads over 8: 184 us and 10 of the join, 0.66 PFLOP/s.  Bound by what two wavefronts to a SIMD do
 // not overlap: per block of 32 keys 1.4 us for the eight of a CU, where the products alone take 0.76, with their
 // operands from LDS 0.97, with the softmax instead 0.98 (one wavefront to a SIMD with 64 rows, half the LDS reads for a
 // product, spills: 293 us; K's products a block ahead of the softmax 201; three to a SIMD spill).
