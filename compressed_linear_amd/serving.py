@@ -270,8 +270,9 @@ class KVCache:
         now = ctypes.c_uint64()
         for key in [k for k in self._work if type(k) is tuple]:
             if _lib.cl_recording(key[0], ctypes.byref(now)) or now.value != key[1]:
-                del self._work[key], self._keep[key]
-                self._recorded -= 1
+                if self._work.pop(key, None):  # another thread may have been here
+                    self._keep.pop(key, None)
+                    self._recorded -= 1
 
     def _workspace(self, sizes, key):
         """Address and bytes of a workspace for these sizes, of a stream or of a recording on it.  An outgrown one can
