@@ -15,8 +15,8 @@ from typing import Optional
 import numpy as np
 
 __all__ = ["ClError", "lib", "pack", "blob_header", "CompressedLinear", "fit_lut", "fit_int", "quant_absmax", "LIB_PATH",
-           "EXPORTED_SYMBOLS", "PROBE_SYMBOLS", "SERVING_SYMBOLS", "rope_table", "rope", "KVCache", "tree_attention",
-           "token_logprobs"]
+           "EXPORTED_SYMBOLS", "PROBE_SYMBOLS", "SERVING_SYMBOLS", "INT8_SYMBOLS", "rope_table", "rope", "KVCache", "PagePool",
+           "tree_attention", "token_logprobs", "quantize_rows", "Int8Linear"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libcompressed_linear.so")
 
@@ -30,8 +30,10 @@ EXPORTED_SYMBOLS = [
 PROBE_SYMBOLS = ["cl_probe_read", "cl_probe_read_sink_words", "cl_probe_empty"]
 
 # the operators around the layers (include/cl_serving.h), exported by the same library
-from .serving import (SERVING_SYMBOLS, KVCache, cl_kv_cache, declare as _declare_serving, rope, rope_table,  # noqa: E402
-                      token_logprobs, tree_attention)
+from .serving import (SERVING_SYMBOLS, KVCache, PagePool, cl_kv_cache, cl_page_pool, declare as _declare_serving,  # noqa: E402
+                      rope, rope_table, token_logprobs, tree_attention)
+# the linear layer in 8-bit integers (include/cl_int8.h), exported by the same library
+from .int8 import INT8_SYMBOLS, Int8Linear, declare as _declare_int8, quantize_rows  # noqa: E402
 
 DENSE = {"lut3": 0, "lut4": 1, "int4": 2, "int8": 3}
 MASK = {"none": 0, "2:4": 1, "bitmap": 2}
@@ -142,6 +144,7 @@ def lib():
         L.cl_probe_empty.argtypes = [ctypes.c_void_p]
         L.cl_probe_empty.restype = ctypes.c_int
         _declare_serving(L)
+        _declare_int8(L)
         _lib = L
     return _lib
 

@@ -1,8 +1,9 @@
-// call.cpp -- entries of cl_serving.h with their arguments in an array.
+// call.cpp -- entries of cl_serving.h and cl_int8.h with their arguments in an array.
 #include <cstring>
 #include <type_traits>
 #include <utility>
 
+#include "cl_int8.h"
 #include "cl_serving.h"
 #include "internal.h"
 
@@ -49,6 +50,17 @@ extern "C" cl_status cl_call(int32_t entry, const int64_t* args) {
     case CL_CALL_KV_READ: return spread(cl_kv_read, args);
     case CL_CALL_TREE_ATTENTION: return spread(cl_tree_attention, args);
     case CL_CALL_TOKEN_LOGPROBS: return spread(cl_token_logprobs, args);
+    case CL_CALL_ROPE_AXES: return spread(cl_rope_axes, args);
+    case CL_CALL_KV_APPEND_AXES: return spread(cl_kv_append_axes, args);
+    case CL_CALL_KV_COPY_PAGES: return spread(cl_kv_copy_pages, args);
+    case CL_CALL_KV_KEEP: return spread(cl_kv_keep, args);
+    case CL_CALL_POOL_EXTEND: return spread(cl_pool_extend, args);
+    case CL_CALL_POOL_FORK: return spread(cl_pool_fork, args);
+    case CL_CALL_POOL_TRUNCATE: return spread(cl_pool_truncate, args);
+    case CL_CALL_POOL_COMPACT: return spread(cl_pool_compact, args);
+    case CL_CALL_INT8_QUANT: return spread(cl_int8_quant, args);
+    case CL_CALL_INT8_LINEAR: return spread(cl_int8_linear, args);
+    case CL_CALL_INT8_FORWARD: return spread(cl_int8_forward, args);
     default: return cl::fail(CL_EINVAL, "call: unknown entry %d", entry);
   }
 }

@@ -40,6 +40,14 @@ __device__ __forceinline__ void pair_of(int layout, int half, int i, int* a, int
   *b = layout == CL_ROPE_HALF ? i + half : 2 * i + 1;
 }
 
+// The axis of each pair, two bits to a pair, eight pairs to a half-word; positions are [axes, stride].  `used` has the bits of the
+// axes that have pairs.
+struct AxisMap {
+  int64_t stride;
+  int axes, used;
+  uint16_t of[64];
+};
+
 struct RopeArgs {
   const void* x;
   void* y;
@@ -47,10 +55,13 @@ struct RopeArgs {
   const float2* table;
   int64_t x_token, x_head, y_token, y_head;
   int tokens, heads, dim, rot, layout, table_rows;
+  AxisMap axes;  // read with several axes only
 };
 
+__device__ __forceinline__ int axis_of(const AxisMap& m, int pair) { return m.of[pair >> 3] >> (2 * (pair & 7)) & 3; }
+
 // Any alignment: one thread a pair of channels, rotated or copied.
-template <int IN, int OUT>
+template <int IN, int OUT, bool AXES>
 __global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
   const int pairs = (a.dim + 1) / 2, half = a.rot / 2;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -67,7 +78,7 @@ __global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
   }
   float u = Elem<IN>::up(x[c1]), v = Elem<IN>::up(x[c2]);
   if (i < half) {
-    const int p = a.positions[t];
+    const int p = a.positions[AXES ? axis_of(a.axes, i) * a.axes.stride + t : t];
     const bool in = p >= 0 && p < a.table_rows;
     const float2 cs = in ? a.table[(int64_t)p * half + i] : make_float2(kNan, kNan);
     rotate_pair(u, v, cs.x, cs.y);
@@ -79,8 +90,8 @@ __global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
 // 16-byte pieces: a thread owns 16 channels of a head -- eight pairs, as two runs of 8 channels in either layout, or
 // 16 channels that are copied -- of HEADS heads of a token, which then load its cosines and sines (from the caches for all
 // heads but one) once.  Bound by memory, a step by the launch (72 heads of 128, fp32 to bf16: one token 2.4 us, 8192 tokens
-// 81 us, 5.7 TB/s).
-template <int IN, int OUT, int HEADS>
+// 81 us, 5.7 TB/s).  With several axes eight pairs of one axis are read as before, others pair by pair.
+template <int IN, int OUT, int HEADS, bool AXES>
 __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   const int units = a.dim / 16, half = a.rot / 2, groups = (a.heads + HEADS - 1) / HEADS;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -90,7 +101,9 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   const bool turned = 16 * u < a.rot;
   int c1 = 16 * u, c2 = c1 + 8;
   if (turned && a.layout == CL_ROPE_HALF) c1 = 8 * u, c2 = c1 + half;
-  const int p = turned ? a.positions[t] : 0;
+  const uint32_t of = AXES && turned ? a.axes.of[u] : 0;  // the axes of pairs 8u to 8u + 7
+  const bool one = !AXES || of == (of & 3) * 0x5555;
+  const int p = !turned ? 0 : AXES ? a.positions[(of & 3) * a.axes.stride + t] : a.positions[t];
   const auto* x = static_cast<const typename Elem<IN>::raw*>(a.x) + t * a.x_token + h * a.x_head;
   auto* y = static_cast<typename Elem<OUT>::raw*>(a.y) + t * a.y_token + h * a.y_head;
   float v1[HEADS][8], v2[HEADS][8];
@@ -102,7 +115,13 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   }
   if (turned) {
     float2 cs[8];
-    if (p >= 0 && p < a.table_rows) {
+    if (AXES && !one) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int q = a.positions[(of >> (2 * i) & 3) * a.axes.stride + t];
+        cs[i] = q >= 0 && q < a.table_rows ? a.table[(int64_t)q * half + 8 * u + i] : make_float2(kNan, kNan);
+      }
+    } else if (p >= 0 && p < a.table_rows) {
       const float4* row = reinterpret_cast<const float4*>(a.table + (int64_t)p * half + 8 * u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -144,7 +163,15 @@ struct AppendArgs {
   const int32_t* positions;
   const float2* table;  // NULL: no rotation
   int tokens, rot, layout, table_rows, page_shift, side;
+  AxisMap axes;  // read with several axes only
 };
+
+// The cosine and sine of pair i of a token whose positions lie in the table.
+template <bool AXES>
+__device__ __forceinline__ float2 cos_sin(const AppendArgs& a, const float2* row, int t, int i) {
+  if constexpr (!AXES) return row[i];
+  return a.table[(int64_t)a.positions[axis_of(a.axes, i) * a.axes.stride + t] * (a.rot / 2) + i];
+}
 
 // Eight channels from `at` of a head at x; VEC: as two 16-byte (fp32) or one load, otherwise one by one.
 template <int IN, bool VEC>
@@ -173,7 +200,7 @@ __device__ __forceinline__ float lanes_max(float v) {
 // D / 8 lanes a (token, head, k or v), eight channels each; heads side by side in a workgroup as in the read, since the inputs are the
 // larger part of the bytes and a token's heads lie together there (8192 tokens of 32 fp32 heads of 128, rotated, to int8: 71 us
 // with 16 heads, 80 with 4, 83 with one).  Bound by memory for prompts, by the launch for steps.
-template <int IN, int KIND, int D, bool VEC>
+template <int IN, int KIND, int D, bool VEC, bool AXES>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   constexpr int LANES = D / 8;
   const int row_at = threadIdx.x / LANES, h = (blockIdx.y << a.side) + (row_at & ((1 << a.side) - 1)), which = blockIdx.z;
@@ -186,9 +213,19 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   float v[8];
   channels8<IN, VEC>(x, ch, v);
   if (a.table && which == 0) {
-    const int p = a.positions[t], half = a.rot / 2;
-    const bool in = p >= 0 && p < a.table_rows;
-    const float2* cs = a.table + (int64_t)(in ? p : 0) * half;
+    const int half = a.rot / 2;
+    const float2* cs = a.table;  // one axis: the position's row
+    bool in = true;
+    if constexpr (AXES) {
+      for (int k = 0; k < a.axes.axes; ++k) {
+        const int p = a.positions[k * a.axes.stride + t];
+        in = in && (!(a.axes.used >> k & 1) || (p >= 0 && p < a.table_rows));
+      }
+    } else {
+      const int p = a.positions[t];
+      in = p >= 0 && p < a.table_rows;
+      cs += (int64_t)(in ? p : 0) * half;
+    }
     if (!in) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -199,7 +236,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
         channels8<IN, VEC>(x, low ? ch + half : ch - half, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 c = cs[(low ? ch : ch - half) + i];
+          const float2 c = cos_sin<AXES>(a, cs, t, (low ? ch : ch - half) + i);
           float p1 = low ? v[i] : w[i], p2 = low ? w[i] : v[i];
           rotate_pair(p1, p2, c.x, c.y);
           v[i] = low ? p1 : p2;
@@ -209,7 +246,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
       if (ch < a.rot) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 c = cs[ch / 2 + i];
+          const float2 c = cos_sin<AXES>(a, cs, t, ch / 2 + i);
           rotate_pair(v[2 * i], v[2 * i + 1], c.x, c.y);
         }
       }
@@ -221,7 +258,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
         int c1, c2;
         pair_of(a.layout, half, pr, &c1, &c2);
         float p1 = Elem<IN>::up(x[c1]), p2 = Elem<IN>::up(x[c2]);
-        rotate_pair(p1, p2, cs[pr].x, cs[pr].y);
+        const float2 c = cos_sin<AXES>(a, cs, t, pr);
+        rotate_pair(p1, p2, c.x, c.y);
         v[i] = ch + i == c1 ? p1 : p2;
       }
     }
@@ -334,14 +372,23 @@ void launch_rope(const RopeArgs& a, hipStream_t s) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)((count * each + 255) / 256)), dim3(256), 0, s, piece_of(a, IN, OUT, first, count));
     });
   };
+  if (a.axes.axes > 1) {
+    if (!vec)
+      go(rope_pair_kernel<IN, OUT, true>, (int64_t)a.heads * ((a.dim + 1) / 2));
+    else if (IN != CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17))
+      go(rope_kernel<IN, OUT, 2, true>, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
+    else
+      go(rope_kernel<IN, OUT, 1, true>, (int64_t)a.heads * (a.dim / 16));
+    return;
+  }
   if (!vec)
-    go(rope_pair_kernel<IN, OUT>, (int64_t)a.heads * ((a.dim + 1) / 2));
+    go(rope_pair_kernel<IN, OUT, false>, (int64_t)a.heads * ((a.dim + 1) / 2));
   // Two heads to a thread for many tokens of 16 bits, whose heads are no larger than the cosines and sines (8192 x 72 heads, half
   // of each rotated: 53 us, 55.5 with one and 54 with four; fp32 83 against 81.5; 64 tokens 3.3 against 3.0).
   else if (IN != CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17))
-    go(rope_kernel<IN, OUT, 2>, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
+    go(rope_kernel<IN, OUT, 2, false>, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
   else
-    go(rope_kernel<IN, OUT, 1>, (int64_t)a.heads * (a.dim / 16));
+    go(rope_kernel<IN, OUT, 1, false>, (int64_t)a.heads * (a.dim / 16));
 }
 
 template <int IN>
@@ -366,10 +413,10 @@ void launch_append(const AppendArgs& a, hipStream_t s) {
     if (a.table) b.positions += first;
     b.tokens = (int)count;
     const dim3 grid((unsigned)((count + each - 1) / each), a.c.heads >> a.side, 2);
-    if (vec)
-      hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, true>), grid, dim3(256), 0, s, b);
-    else
-      hipLaunchKernelGGL((kv_append_kernel<IN, KIND, D, false>), grid, dim3(256), 0, s, b);
+    const bool axes = a.table && a.axes.axes > 1;
+    const auto kernel = axes ? (vec ? kv_append_kernel<IN, KIND, D, true, true> : kv_append_kernel<IN, KIND, D, false, true>)
+                             : (vec ? kv_append_kernel<IN, KIND, D, true, false> : kv_append_kernel<IN, KIND, D, false, false>);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, b);
   });
 }
 
@@ -456,10 +503,54 @@ extern "C" cl_status cl_rope_table(int32_t positions, int32_t rot, double base, 
   return launched("rope table");
 }
 
+namespace {
+
+// The axis of every pair of a rotation over `rot` channels; no sections: one axis.
+cl_status axis_map(const int32_t* sections, int axes, int order, int rot, int tokens, AxisMap* m) {
+  *m = AxisMap{tokens, 1, 1, {}};
+  if (!sections) return CL_OK;
+  if (axes < 1 || axes > 4) return fail(CL_EINVAL, "rope: %d axes (1 to 4 are wanted)", axes);
+  if (order != CL_ROPE_BLOCKS && order != CL_ROPE_TURNS) return fail(CL_EINVAL, "rope: unknown order %d of the axes", order);
+  const int half = rot / 2;
+  int64_t sum = 0;
+  for (int k = 0; k < axes; ++k) {
+    if (sections[k] < 0) return fail(CL_EINVAL, "rope: a section of %d pairs", sections[k]);
+    sum += sections[k];
+    if (order == CL_ROPE_TURNS && k && sections[k] && k + (int64_t)axes * (sections[k] - 1) >= half)
+      return fail(CL_EINVAL, "rope: axis %d does not get %d turns among %d pairs", k, sections[k], half);
+  }
+  if (sum != half) return fail(CL_EINVAL, "rope: sections of %lld pairs, the table has %d", (long long)sum, half);
+  m->axes = axes;
+  m->used = 0;
+  for (int i = 0, k = 0, end = sections[0]; i < half; ++i) {
+    int axis = i % axes;
+    if (order == CL_ROPE_BLOCKS) {
+      while (i >= end) end += sections[++k];
+      axis = k;
+    } else if (i / axes >= sections[axis]) {
+      axis = 0;
+    }
+    m->of[i / 8] |= (uint16_t)(axis << (2 * (i % 8)));
+    m->used |= 1 << axis;
+  }
+  return CL_OK;
+}
+
+}  // namespace
+
 extern "C" cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, int64_t x_head, int32_t tokens,
                              int32_t heads, int32_t dim, const int32_t* positions, const float* table,
                              int32_t table_rows, int32_t rot, int32_t layout, void* y, int32_t y_dtype, int64_t y_token,
                              int64_t y_head, void* stream) {
+  return cl_rope_axes(x, x_dtype, x_token, x_head, tokens, heads, dim, positions, 1, nullptr, CL_ROPE_BLOCKS, table, table_rows,
+                      rot, layout, y, y_dtype, y_token, y_head, stream);
+}
+
+extern "C" cl_status cl_rope_axes(const void* x, int32_t x_dtype, int64_t x_token, int64_t x_head, int32_t tokens,
+                                  int32_t heads, int32_t dim, const int32_t* positions, int32_t axes,
+                                  const int32_t* sections, int32_t order, const float* table, int32_t table_rows,
+                                  int32_t rot, int32_t layout, void* y, int32_t y_dtype, int64_t y_token, int64_t y_head,
+                                  void* stream) {
   clear_error();
   if (tokens < 0 || heads < 1 || dim < 2) return fail(CL_EINVAL, "rope: tokens >= 0, heads >= 1 and dim >= 2 are wanted");
   if (!elem_ok(x_dtype) || !elem_ok(y_dtype)) return fail(CL_EINVAL, "rope: unknown element type");
@@ -473,8 +564,9 @@ extern "C" cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, in
   if (y == x && (x_dtype != y_dtype || x_token != y_token || x_head != y_head))
     return fail(CL_EINVAL, "rope: y may be x only with the same type and strides");
   if ((int64_t)tokens * heads >= ((int64_t)1 << 40) / dim) return fail(CL_ESIZE, "rope: tokens * heads * dim at 2^40 or more");
-  const RopeArgs a = {x, y, positions, reinterpret_cast<const float2*>(table), x_token, x_head, y_token, y_head,
-                      tokens, heads, dim, rot, layout, table_rows};
+  RopeArgs a = {x, y, positions, reinterpret_cast<const float2*>(table), x_token, x_head, y_token, y_head,
+                tokens, heads, dim, rot, layout, table_rows, {}};
+  if ((st = axis_map(sections, axes, order, rot, tokens, &a.axes)) != CL_OK) return st;
   if ((int64_t)heads * ((dim + 1) / 2) > kLaunch) return fail(CL_ESIZE, "rope: too many heads");
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (x_dtype == CL_F16)
@@ -490,6 +582,15 @@ extern "C" cl_status cl_kv_append(const cl_kv_cache* cache, const void* k, const
                                   int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
                                   const int32_t* slots, const int32_t* positions, const float* table,
                                   int32_t table_rows, int32_t rot, int32_t layout, void* stream) {
+  return cl_kv_append_axes(cache, k, v, dtype, tokens, k_token, k_head, v_token, v_head, slots, positions, 1, nullptr,
+                           CL_ROPE_BLOCKS, table, table_rows, rot, layout, stream);
+}
+
+extern "C" cl_status cl_kv_append_axes(const cl_kv_cache* cache, const void* k, const void* v, int32_t dtype,
+                                       int32_t tokens, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                                       const int32_t* slots, const int32_t* positions, int32_t axes,
+                                       const int32_t* sections, int32_t order, const float* table, int32_t table_rows,
+                                       int32_t rot, int32_t layout, void* stream) {
   clear_error();
   cl_status st = check_cache(cache);
   if (st != CL_OK) return st;
@@ -500,8 +601,9 @@ extern "C" cl_status cl_kv_append(const cl_kv_cache* cache, const void* k, const
   if (!aligned_to(k, elem_size(dtype)) || !aligned_to(v, elem_size(dtype)) || !aligned_to(slots, 4))
     return fail(CL_EINVAL, "append: a pointer is misaligned for its type");
   if (table && (st = check_rope(positions, table, table_rows, rot, layout, cache->dim)) != CL_OK) return st;
-  const AppendArgs a = {*cache, {k, v}, {k_token, v_token}, {k_head, v_head}, slots, positions,
-                        reinterpret_cast<const float2*>(table), tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size), heads_side_by_side(cache->heads)};
+  AppendArgs a = {*cache, {k, v}, {k_token, v_token}, {k_head, v_head}, slots, positions, reinterpret_cast<const float2*>(table),
+                  tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size), heads_side_by_side(cache->heads), {}};
+  if (table && (st = axis_map(sections, axes, order, rot, tokens, &a.axes)) != CL_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)
     launch_append<CL_F16>(a, s);

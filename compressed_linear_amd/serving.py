@@ -9,10 +9,13 @@ from __future__ import annotations
 
 import ctypes
 import struct
+from array import array
 from typing import Optional
 
 SERVING_SYMBOLS = ["cl_rope_table", "cl_rope", "cl_kv_append", "cl_kv_read", "cl_tree_attention_work_bytes",
-                   "cl_tree_attention", "cl_recording", "cl_token_logprobs", "cl_call"]
+                   "cl_tree_attention", "cl_recording", "cl_token_logprobs", "cl_call", "cl_rope_axes", "cl_kv_append_axes",
+                   "cl_kv_copy_pages", "cl_kv_keep", "cl_pool_extend", "cl_pool_fork", "cl_pool_truncate",
+                   "cl_pool_compact_work_bytes", "cl_pool_compact"]
 
 
 class UnknownName(ValueError, KeyError):
@@ -27,6 +30,7 @@ class _Names(dict):
 
 
 ROPE_LAYOUT = _Names(half=0, interleaved=1)
+ROPE_ORDER = _Names(blocks=0, turns=1)
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 KV_KIND = {"int8": 0, "int4": 1}
 COUNTER_BYTES = 262144  # CL_ATTENTION_COUNTER_BYTES
@@ -39,6 +43,12 @@ class cl_kv_cache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("kind", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class cl_page_pool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("left_out", ctypes.c_void_p), ("sequences", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
 def declare(L):
@@ -55,6 +65,15 @@ def declare(L):
     L.cl_recording.argtypes = [p, ctypes.POINTER(ctypes.c_uint64)]
     L.cl_token_logprobs.argtypes = [p, i, q, i, i, p, i, p, p, i, p, p, p]
     L.cl_call.argtypes = [i, ctypes.c_char_p]
+    pool = ctypes.POINTER(cl_page_pool)
+    L.cl_rope_axes.argtypes = [p, i, q, q, i, i, i, p, i, p, i, p, i, i, i, p, i, q, q, p]
+    L.cl_kv_append_axes.argtypes = [cache, p, p, i, i, q, q, q, q, p, p, i, p, i, p, i, i, i, p]
+    L.cl_kv_copy_pages.argtypes = [cache, p, p, i, p]
+    L.cl_kv_keep.argtypes = [cache, p, i, i, p, p, i, p]
+    L.cl_pool_extend.argtypes = [pool, p, i, p, p, p, p]
+    L.cl_pool_fork.argtypes = L.cl_pool_truncate.argtypes = [pool, p, p]
+    L.cl_pool_compact_work_bytes.argtypes = [i]
+    L.cl_pool_compact.argtypes = [pool, i, p, p, p, ctypes.c_size_t, p]
     for name in SERVING_SYMBOLS:
         getattr(L, name).restype = ctypes.c_size_t if name.endswith("_bytes") else ctypes.c_int
 
@@ -63,6 +82,9 @@ def declare(L):
 _ROPE, _APPEND, _READ, _ATTENTION, _LOGPROBS = range(5)
 _pack_rope, _pack_append, _pack_read, _pack_attention, _pack_logprobs = (
     struct.Struct(f).pack for f in ("17q", "16q", "7q", "16qd4q", "13q"))
+_ROPE_AXES, _APPEND_AXES, _COPY_PAGES, _KEEP, _EXTEND, _FORK, _TRUNCATE, _COMPACT = range(16, 24)
+_pack_rope_axes, _pack_append_axes, _pack_copy_pages, _pack_keep, _pack_extend, _pack_fork, _pack_compact = (
+    struct.Struct(f).pack for f in ("20q", "19q", "5q", "8q", "7q", "3q", "7q"))
 
 _torch = None
 _lib = None
@@ -125,6 +147,27 @@ def _table(table, dev):
     return table.data_ptr(), shape[0], 2 * shape[1]
 
 
+_sections: dict = {}  # the sections that were used, by their bytes: host arrays and their addresses
+
+
+def _axes(positions, T, sections, dev):
+    """Positions [axes, tokens] and the pairs of each axis: the addresses of both and the number of axes."""
+    try:
+        pairs = array("i", sections)
+    except (TypeError, OverflowError):
+        raise ValueError(f"sections must be the pairs of each axis, not {sections!r}") from None
+    axes = len(pairs)
+    if not 1 <= axes <= 4 or positions.dim() != 2 or positions.shape[0] != axes:
+        raise ValueError(f"positions must be int32 [{axes}, {T}] for sections {tuple(pairs)} (1 to 4 axes)")
+    key = pairs.tobytes()
+    host = _sections.get(key)
+    if host is None:
+        if min(pairs) < 0 or sum(pairs) > 512:
+            raise ValueError("sections are pairs of up to 1024 channels")
+        host = _sections[key] = pairs, pairs.buffer_info()[0]
+    return _index(positions, axes * T, dev, "positions"), axes, host[1]
+
+
 def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                trained: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
     """Cosines and sines of `positions` positions for a rotation over `rot` channels (cl_rope_table): a
@@ -142,11 +185,17 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "
     return out
 
 
-def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None):
+def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None, sections=None, order: str = "blocks"):
     """Rotary positions (cl_rope): x [tokens, heads, dim] float16, bfloat16 or float32 (any token and head
     strides, so a view of a qkv output will do), positions int32 [tokens], table from `rope_table`; the
     first 2 * table.shape[1] channels are rotated, the others copied.  Returns `out`, or a new
-    contiguous tensor of `out_dtype` (x's type by default).  `out` may be x."""
+    contiguous tensor of `out_dtype` (x's type by default).  `out` may be x.
+
+    Positions with several axes (cl_rope_axes; time, height and width of a video, say): `sections` gives the pairs of each of
+    1 to 4 axes, table.shape[1] together, and positions are int32 [axes, tokens].  order 'blocks': the pairs of an axis
+    lie side by side; 'turns': the axes alternate while they have pairs left, the rest is axis 0's.  Frequencies
+    that start anew with each axis are tables of the axes side by side:
+    torch.cat([rope_table(P, 2 * n) for n in sections], 1)."""
     L = _lib or _setup()
     x = _heads3(x, "x")
     dev, shape = x.device, x.shape
@@ -162,6 +211,13 @@ def rope(x, positions, table, layout: str = "half", out=None, out_dtype=None):
     if out.dtype not in _DT:
         raise ValueError("the output must be float16, bfloat16 or float32")
     tp, rows, rot = _table(table, dev)
+    if sections is not None:
+        st = L.cl_call(_ROPE_AXES, _pack_rope_axes(
+            x.data_ptr(), _DT[x.dtype], xt, xh, T, H, D, *_axes(positions, T, sections, dev), ROPE_ORDER[order], tp, rows, rot,
+            ROPE_LAYOUT[layout], out.data_ptr(), _DT[out.dtype], yt, yh, _stream(dev)))
+        if st:
+            _check(st, "cl_rope_axes")
+        return out
     st = L.cl_call(_ROPE, _pack_rope(
         x.data_ptr(), _DT[x.dtype], xt, xh, T, H, D, _index(positions, T, dev, "positions"), tp, rows, rot,
         ROPE_LAYOUT[layout], out.data_ptr(), _DT[out.dtype], yt, yh, _stream(dev)))
@@ -218,10 +274,10 @@ class KVCache:
         self._keep: dict = {}   # their tensors
         self._recorded = 0      # how many of them are recordings'
 
-    def append(self, k, v, slots, positions=None, table=None, layout: str = "half"):
+    def append(self, k, v, slots, positions=None, table=None, layout: str = "half", sections=None, order: str = "blocks"):
         """Quantise new keys and values [tokens, heads, dim] into `slots` (int32 [tokens]; a slot outside the
         cache, -1 say, stores nothing).  With `table` (and int32 `positions`) the keys are rotated on
-        the way, from unrounded results, as `rope` would."""
+        the way, from unrounded results, as `rope` would (`sections` and `order`: positions with several axes)."""
         k, v, dev = _heads3(k, "k"), _heads3(v, "v"), self.device
         shape, dt = k.shape, k.dtype
         if v.shape != shape or v.dtype is not dt or k.device != dev or v.device != dev \
@@ -233,9 +289,18 @@ class KVCache:
             tp, rows, rot = _table(table, dev)
             if positions is None:
                 raise ValueError("a table needs positions")
-            pp = _index(positions, T, dev, "positions")
+            pp = _index(positions, T, dev, "positions") if sections is None else 0
+        elif sections is not None:
+            raise ValueError("sections need a table")
         kt, kh, _ = k.stride()
         vt, vh, _ = v.stride()
+        if sections is not None:
+            st = _lib.cl_call(_APPEND_AXES, _pack_append_axes(
+                self._ref, k.data_ptr(), v.data_ptr(), _DT[dt], T, kt, kh, vt, vh, _index(slots, T, dev, "slots"),
+                *_axes(positions, T, sections, dev), ROPE_ORDER[order], tp, rows, rot, ROPE_LAYOUT[layout], _stream(dev)))
+            if st:
+                _check(st, "cl_kv_append_axes")
+            return
         st = _lib.cl_call(_APPEND, _pack_append(
             self._ref, k.data_ptr(), v.data_ptr(), _DT[dt], T, kt, kh, vt, vh, _index(slots, T, dev, "slots"), pp, tp,
             rows, rot, ROPE_LAYOUT[layout], _stream(dev)))
@@ -256,6 +321,30 @@ class KVCache:
         if st:
             _check(st, "cl_kv_read")
         return k, v
+
+    def copy_pages(self, src, dst):
+        """Copies whole pages inside the cache (cl_kv_copy_pages): page src[i] to page dst[i] (int32 [n] both; an entry with
+        either outside the cache, -1 say, copies nothing), as PagePool's `extend` and `compact` want it."""
+        dev, n = self.device, src.numel()
+        st = _lib.cl_call(_COPY_PAGES, _pack_copy_pages(self._ref, _index(src, n, dev, "src"), _index(dst, n, dev, "dst"), n,
+                                                        _stream(dev)))
+        if st:
+            _check(st, "cl_kv_copy_pages")
+
+    def keep(self, block_table, ctx_lens, kept):
+        """Moves accepted drafts together (cl_kv_keep): the entries of draft kept[b, j] (int32 [sequences, most], most
+        at most 256, -1: none) of sequence b, whose drafts lie after its ctx_lens[b] tokens, are copied to the place of its
+        draft j.  A sequence's drafts are all read before any is written."""
+        dev = self.device
+        if block_table.dim() != 2 or kept.dim() != 2 or kept.shape[0] != block_table.shape[0]:
+            raise ValueError("block_table must be int32 [sequences, width] and kept int32 [sequences, most]")
+        B, width = block_table.shape
+        most = kept.shape[1]
+        st = _lib.cl_call(_KEEP, _pack_keep(
+            self._ref, _index(block_table, B * width, dev, "block_table"), width, B, _index(ctx_lens, B, dev, "ctx_lens"),
+            _index(kept, B * most, dev, "kept"), most, _stream(dev)))
+        if st:
+            _check(st, "cl_kv_keep")
 
     def _recording(self, stream):
         """Whose workspace a call that is recorded on `stream` takes.  It is the recording's even where the stream has
@@ -287,6 +376,93 @@ class KVCache:
             self._recorded += 1
         self._work[key] = work.data_ptr(), size
         return self._work[key]
+
+
+class PagePool:
+    """Which sequence holds which pages (cl_page_pool), for any caches of one page size on one GPU: block_table int32
+    [sequences, width] (a sequence's pages, -1 past the last), lens int32 [sequences] (its tokens), refs int32 [pages] (how
+    often a page stands in the table; 0: free) and left_out int32 [1] (sequences that the last `extend` found no room for).
+
+    Either sizes are given, and all pages are free, or the three tensors are.  Every operation runs on the GPU in its
+    stream's order and can be recorded; the tensors stay where they are.
+    """
+
+    def __init__(self, pages: int = 0, page_size: int = 64, sequences: int = 1, width: int = 1, device=None,
+                 block_table=None, lens=None, refs=None):
+        _setup()
+        torch = _torch
+        three = (block_table, lens, refs)
+        if all(t is None for t in three):
+            if pages < 1 or sequences < 1 or width < 1:
+                raise ValueError("pages, sequences and width are at least 1")
+            dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+            block_table = torch.full((sequences, width), -1, dtype=torch.int32, device=dev)
+            lens, refs = (torch.zeros(n, dtype=torch.int32, device=dev) for n in (sequences, pages))
+        elif any(t is None for t in three):
+            raise ValueError("block_table, lens and refs are given together")
+        if block_table.dim() != 2 or refs.dim() != 1 or tuple(lens.shape) != (block_table.shape[0],):
+            raise ValueError("block_table must be int32 [sequences, width], lens int32 [sequences], refs int32 [pages]")
+        for t in (block_table, lens, refs):
+            if t.dtype is not torch.int32 or t.device != block_table.device or not t.is_cuda or not t.is_contiguous():
+                raise ValueError("a pool's tensors must be contiguous int32 tensors on one ROCm device")
+        self.block_table, self.lens, self.refs = block_table, lens, refs
+        self.device = block_table.device
+        self.sequences, self.width = block_table.shape
+        self.pages, self.page_size = refs.numel(), page_size
+        self.left_out = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._desc = cl_page_pool(block_table.data_ptr(), lens.data_ptr(), refs.data_ptr(), self.left_out.data_ptr(),
+                                  self.sequences, self.width, self.pages, page_size)
+        self._ref = ctypes.addressof(self._desc)
+
+    def extend(self, cu_q, tokens: int):
+        """Room for new tokens (cl_pool_extend): sequence b gets cu_q[b + 1] - cu_q[b] (int32 [sequences + 1], as for
+        `tree_attention`), `tokens` in all.  Returns (slots int32 [tokens], src, dst int32 [sequences]): the tokens'
+        places, for KVCache.append, and the pages that KVCache.copy_pages has to copy before, in every cache, since
+        other sequences hold them too.  A sequence that there is no room for stays as it was, its slots are -1, and
+        left_out counts it."""
+        dev = self.device
+        if tokens < 0:
+            raise ValueError("tokens must be >= 0")
+        B = self.sequences
+        buf = _empty(tokens + 2 * B, dtype=_i32, device=dev)
+        at = buf.data_ptr()
+        st = _lib.cl_call(_EXTEND, _pack_extend(self._ref, _index(cu_q, B + 1, dev, "cu_q"), tokens, at, at + 4 * tokens,
+                                                at + 4 * (tokens + B), _stream(dev)))
+        if st:
+            _check(st, "cl_pool_extend")
+        return buf[:tokens], buf[tokens:tokens + B], buf[tokens + B:]
+
+    def fork(self, parents):
+        """Every sequence b at once becomes what sequence parents[b] (int32 [sequences]) was, sharing its pages
+        (cl_pool_fork); parents[b] == b stays, -1 ends and gives its pages back."""
+        dev = self.device
+        st = _lib.cl_call(_FORK, _pack_fork(self._ref, _index(parents, self.sequences, dev, "parents"), _stream(dev)))
+        if st:
+            _check(st, "cl_pool_fork")
+
+    def truncate(self, lens):
+        """Sequences shortened to lens[b] tokens (int32 [sequences]; 0 frees a sequence, -1 leaves it), the pages past them
+        given back (cl_pool_truncate)."""
+        dev = self.device
+        st = _lib.cl_call(_TRUNCATE, _pack_fork(self._ref, _index(lens, self.sequences, dev, "lens"), _stream(dev)))
+        if st:
+            _check(st, "cl_pool_truncate")
+
+    def compact(self, max_moves: Optional[int] = None):
+        """Moves the highest pages that are held to the lowest free ones (cl_pool_compact), at most max_moves of them (all
+        by default).  Returns (src, dst) int32 [max_moves], -1 past the last: KVCache.copy_pages has to copy them in
+        every cache."""
+        dev = self.device
+        n = self.pages if max_moves is None else max_moves
+        if n < 0:
+            raise ValueError("max_moves must be >= 0")
+        size = 4 * (self.pages + 1)
+        buf = _empty(2 * n + self.pages + 1, dtype=_i32, device=dev)
+        at = buf.data_ptr()
+        st = _lib.cl_call(_COMPACT, _pack_compact(self._ref, n, at, at + 4 * n, at + 8 * n, size, _stream(dev)))
+        if st:
+            _check(st, "cl_pool_compact")
+        return buf[:n], buf[n:2 * n]
 
 
 def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, max_ctx: Optional[int] = None,

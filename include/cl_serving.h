@@ -24,6 +24,8 @@ extern "C" {
 typedef enum { CL_F16 = 0, CL_BF16 = 1, CL_F32 = 2 } cl_dtype;
 /* Pairs of a rotation over `rot` channels: HALF (i, i + rot/2), INTERLEAVED (2i, 2i + 1). */
 typedef enum { CL_ROPE_HALF = 0, CL_ROPE_INTERLEAVED = 1 } cl_rope_layout;
+/* Which axis a pair belongs to, where positions have several: BLOCKS the pairs of an axis lie side by side, TURNS the axes alternate. */
+typedef enum { CL_ROPE_BLOCKS = 0, CL_ROPE_TURNS = 1 } cl_rope_order;
 /* How rotation angles are scaled for contexts past the trained length. */
 typedef enum { CL_ROPE_NONE = 0, CL_ROPE_LINEAR = 1, CL_ROPE_NTK = 2, CL_ROPE_YARN = 3 } cl_rope_scaling;
 typedef enum { CL_KV_INT8 = 0, CL_KV_INT4 = 1 } cl_kv_kind;
@@ -63,6 +65,25 @@ cl_status cl_rope_table(int32_t positions, int32_t rot, double base, int32_t sca
 cl_status cl_rope(const void* x, int32_t x_dtype, int64_t x_token, int64_t x_head, int32_t tokens, int32_t heads,
                   int32_t dim, const int32_t* positions, const float* table, int32_t table_rows, int32_t rot,
                   int32_t layout, void* y, int32_t y_dtype, int64_t y_token, int64_t y_head, void* stream);
+
+/*
+ * cl_rope_axes -- cl_rope for positions with several axes (time, height and width of a video, say): pair i of a
+ * token is rotated by the table row of the token's position on the pair's axis a(i).
+ *   positions        device, [axes, tokens] int32; a position outside [0, table_rows) gives NaN in the pairs of its
+ *                    axis
+ *   axes, sections   1 to 4; host, [axes] int32, the pairs of each axis (0 is allowed), rot / 2 together.
+ *                    sections NULL: one axis, the others are not read
+ *   order            BLOCKS  the first sections[0] pairs belong to axis 0, the next sections[1] to axis 1, and so on;
+ *                    TURNS   a(i) = i % axes while i / axes < sections[i % axes], otherwise axis 0
+ * A table whose frequencies start anew with each axis (an image's height and width) is one whose columns are those of
+ * several cl_rope_table side by side.
+ * Errors: as cl_rope; CL_EINVAL for sections that are negative, do not add up to rot / 2, or do not get all their
+ * turns.
+ */
+cl_status cl_rope_axes(const void* x, int32_t x_dtype, int64_t x_token, int64_t x_head, int32_t tokens, int32_t heads,
+                       int32_t dim, const int32_t* positions, int32_t axes, const int32_t* sections, int32_t order,
+                       const float* table, int32_t table_rows, int32_t rot, int32_t layout, void* y, int32_t y_dtype,
+                       int64_t y_token, int64_t y_head, void* stream);
 
 /*
  * A paged, quantised K/V cache in caller-owned device memory.  Slot s is place s % page_size of page
@@ -108,6 +129,16 @@ cl_status cl_kv_append(const cl_kv_cache* cache, const void* k, const void* v, i
                        void* stream);
 
 /*
+ * cl_kv_append_axes -- cl_kv_append for positions with several axes; positions, axes, sections, order as in
+ * cl_rope_axes.  A key with a position outside the table on an axis that has pairs is stored as zeros.
+ * Errors: as cl_kv_append and cl_rope_axes.
+ */
+cl_status cl_kv_append_axes(const cl_kv_cache* cache, const void* k, const void* v, int32_t dtype, int32_t tokens,
+                            int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, const int32_t* slots,
+                            const int32_t* positions, int32_t axes, const int32_t* sections, int32_t order,
+                            const float* table, int32_t table_rows, int32_t rot, int32_t layout, void* stream);
+
+/*
  * cl_kv_read -- the stored values of n slots: k_out[i], v_out[i] [heads, dim] = code * scale of slot
  * slots[i], rounded once to `dtype`; zeros for a slot outside the cache.
  *   k_out, v_out     device, [n, heads, dim] contiguous, 16-byte aligned; slots device, [n] int32.
@@ -115,6 +146,96 @@ cl_status cl_kv_append(const cl_kv_cache* cache, const void* k, const void* v, i
  */
 cl_status cl_kv_read(const cl_kv_cache* cache, const int32_t* slots, int32_t n, void* k_out, void* v_out,
                      int32_t dtype, void* stream);
+
+/*
+ * cl_kv_copy_pages -- whole pages copied inside a cache: page src[i] to page dst[i], codes and scales of K and V.
+ *   src, dst         device, [n] int32.  An entry with either outside [0, pages) (-1, say) copies nothing.  No page is the
+ *                    destination of two entries, or of one and the source of another.
+ * Scales must be 16-byte aligned.
+ * Errors: CL_EINVAL (a malformed cache, n < 0, NULL or misaligned pointers), CL_EUNSUPPORTED (dim), CL_ESIZE, CL_EHIP.
+ */
+cl_status cl_kv_copy_pages(const cl_kv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/*
+ * cl_kv_keep -- accepted drafts moved together.  Sequence b has ctx_lens[b] tokens, followed in the cache by its drafts;
+ * for each j with i = kept[b][j] >= 0 the entries of draft i (place ctx_lens[b] + i) are copied to place
+ * ctx_lens[b] + j, codes and scales as they are.  All of a sequence's drafts are read before any is written, so kept may be
+ * any list, in any order.
+ *   block_table      device, [sequences, table_width] int32, as in cl_tree_attention
+ *   ctx_lens, kept   device, [sequences] and [sequences, most] int32, most <= 256
+ * A place past the table's width or whose page lies outside the cache is neither read nor written.  The places
+ * written belong to their sequence alone (cl_pool_extend sees to that).
+ * Errors: CL_EINVAL, CL_EUNSUPPORTED (dim, most), CL_ESIZE, CL_EHIP.
+ */
+cl_status cl_kv_keep(const cl_kv_cache* cache, const int32_t* block_table, int32_t table_width, int32_t sequences,
+                     const int32_t* ctx_lens, const int32_t* kept, int32_t most, void* stream);
+
+/*
+ * Which sequence holds which pages, in caller-owned device memory.  The pages are numbers: any caches of the same page
+ * size (a model's layers, say) share a pool.
+ *   block_table      [sequences, width] int32: a sequence's pages in their order, -1 past the last
+ *   lens             [sequences] int32: its tokens
+ *   refs             [pages] int32: how many times a page stands in the table; 0: it is free
+ *   left_out         [1] int32, written by cl_pool_extend
+ * A sequence of n tokens has ceil(n / page_size) pages.  At the start the table is -1, lens and refs 0.  A program
+ * may hold a page itself by adding to its refs.
+ * page_size is a power of two in [16, 1024]; sequences <= 4096; pages * page_size and width * page_size < 2^31.  One
+ * call at a time may use a pool; its operations and everything that reads it run in the stream's order.
+ */
+typedef struct {
+  int32_t* block_table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* left_out;
+  int32_t sequences, width, pages, page_size;
+} cl_page_pool;
+
+/*
+ * cl_pool_extend -- room for new tokens: sequence b gets n_b = cu_q[b+1] - cu_q[b] more, and pages for them, its last page
+ * among them if other sequences hold that too and its tokens do not fill it (it has to be copied then).  Of a
+ * page whose holders are all extended the last one keeps it.  Free pages are given out lowest first, to
+ * sequences in their order and to each one's places in their order.
+ *   cu_q             device, [sequences + 1] int32, as in cl_tree_attention
+ *   slots            device, [tokens] int32: the new tokens' slots, for cl_kv_append; -1 for tokens of no sequence and
+ *                    of those left out
+ *   src, dst         device, [sequences] int32: the page to copy (cl_kv_copy_pages, in every cache, before anything is
+ *                    appended), -1 where there is none
+ * A sequence whose cu_q does not fit [0, tokens] or begins below an earlier number of cu_q, whose table is too narrow or whose
+ * last page is no page is left out and stays as it was; so is one for which the free pages do not suffice, and every one after it that gets tokens.
+ * left_out is how many there are.
+ * Errors: CL_EINVAL, CL_ESIZE, CL_EHIP.
+ */
+cl_status cl_pool_extend(const cl_page_pool* pool, const int32_t* cu_q, int32_t tokens, int32_t* slots, int32_t* src,
+                         int32_t* dst, void* stream);
+
+/*
+ * cl_pool_fork -- every sequence b at once becomes what sequence parents[b] was, sharing its pages: parents[b] == b
+ * stays, -1 (any number that is no sequence) ends and gives its pages back.
+ *   parents          device, [sequences] int32
+ * Errors: CL_EINVAL, CL_ESIZE, CL_EHIP.
+ */
+cl_status cl_pool_fork(const cl_page_pool* pool, const int32_t* parents, void* stream);
+
+/*
+ * cl_pool_truncate -- sequences shortened to lens[b] tokens, the pages past them given back; a negative number or
+ * one that is not below the sequence's leaves it.
+ *   lens             device, [sequences] int32, not the pool's own
+ * Errors: CL_EINVAL, CL_ESIZE, CL_EHIP.
+ */
+cl_status cl_pool_truncate(const cl_page_pool* pool, const int32_t* lens, void* stream);
+
+/*
+ * cl_pool_compact -- the highest pages that are held move to the lowest free ones, while those are lower: after enough moves
+ * the n pages that are held are 0 to n - 1.  The table and refs are changed; the pages are to be copied
+ * (cl_kv_copy_pages, in every cache).
+ *   max_moves        at most this many pages move
+ *   src, dst         device, [max_moves] int32: the moves, highest source first; -1 past the last
+ *   work             device, cl_pool_compact_work_bytes(pages) bytes
+ * Errors: CL_EINVAL, CL_ESIZE, CL_ENOMEM (work_bytes too small), CL_EHIP.
+ */
+size_t cl_pool_compact_work_bytes(int32_t pages);
+cl_status cl_pool_compact(const cl_page_pool* pool, int32_t max_moves, int32_t* src, int32_t* dst, void* work,
+                          size_t work_bytes, void* stream);
 
 /*
  * cl_tree_attention -- attention of each sequence's newest tokens over its cached keys and values.
@@ -188,12 +309,15 @@ cl_status cl_token_logprobs(const void* x, int32_t dtype, int64_t x_row, int32_t
                             int32_t* top_ids, float* top_logp, void* stream);
 
 /*
- * cl_call -- calls cl_rope, cl_kv_append, cl_kv_read, cl_tree_attention or cl_token_logprobs with its
- * arguments in an array, in their order: pointers and integers as 64-bit integers, the scale as the bits of a
+ * cl_call -- calls cl_rope, cl_kv_append, cl_kv_read, cl_tree_attention, cl_token_logprobs or an entry of the second list with
+ * its arguments in an array, in their order: pointers and integers as 64-bit integers, a float as the bits of a
  * double.  For bindings that pay for every argument of a foreign call.
  * Errors: the entry's; CL_EINVAL for an unknown entry or args NULL.
  */
 enum { CL_CALL_ROPE = 0, CL_CALL_KV_APPEND = 1, CL_CALL_KV_READ = 2, CL_CALL_TREE_ATTENTION = 3, CL_CALL_TOKEN_LOGPROBS = 4 };
+enum { CL_CALL_ROPE_AXES = 16, CL_CALL_KV_APPEND_AXES = 17, CL_CALL_KV_COPY_PAGES = 18, CL_CALL_KV_KEEP = 19,
+       CL_CALL_POOL_EXTEND = 20, CL_CALL_POOL_FORK = 21, CL_CALL_POOL_TRUNCATE = 22, CL_CALL_POOL_COMPACT = 23,
+       CL_CALL_INT8_QUANT = 24, CL_CALL_INT8_LINEAR = 25, CL_CALL_INT8_FORWARD = 26 /* cl_int8.h */ };
 cl_status cl_call(int32_t entry, const int64_t* args);
 
 #ifdef __cplusplus
