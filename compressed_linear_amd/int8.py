@@ -16,15 +16,15 @@ INT8_SYMBOLS = ["cl_int8_quant", "cl_int8_linear", "cl_int8_work_bytes", "cl_int
 MOST_K = 131071
 
 _QUANT, _LINEAR, _FORWARD = 24, 25, 26
-_pack_quant, _pack_linear, _pack_forward = (struct.Struct(f).pack for f in ("5qd4q", "14q", "4qd12q"))
+_pack_quant, _pack_linear, _pack_forward = (struct.Struct(f).pack for f in ("5qd4q", "16q", "4qd12q"))
 
 
 def declare(L):
     """Argument types of the entry points, on the loaded library."""
     p, i, q, f, z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     L.cl_int8_quant.argtypes = [p, i, q, i, i, f, p, q, p, p]
-    L.cl_int8_linear.argtypes = [p, q, p, i, p, q, p, p, i, i, p, i, q, p]
-    L.cl_int8_work_bytes.argtypes = [i, i]
+    L.cl_int8_linear.argtypes = [p, q, p, i, p, q, p, p, i, i, p, i, q, p, z, p]
+    L.cl_int8_work_bytes.argtypes = [i, i, i, i]
     L.cl_int8_forward.argtypes = [p, i, q, i, f, p, q, p, p, i, i, p, i, q, p, z, p]
     for name in INT8_SYMBOLS:
         getattr(L, name).restype = z if name.endswith("_bytes") else ctypes.c_int
@@ -83,7 +83,7 @@ def _whole_rows(codes):
     if T == 1:
         row = max(row, _padded(K)) // 128 * 128
     end = codes.storage_offset() + (T - 1) * row + _padded(K)
-    return (one == 1 or K == 1) and row % 128 == 0 and row >= K and codes.data_ptr() % 16 == 0 \
+    return (one == 1 or K == 1) and row % 128 == 0 and K <= row <= 1 << 23 and codes.data_ptr() % 16 == 0 \
         and end <= codes.untyped_storage().nbytes(), row
 
 
@@ -148,7 +148,7 @@ class Int8Linear:
         x, row = _rows2(x, self.K, dev, "x")
         T = x.shape[0]
         y, yp, yd, yr = self._output(T, out, out_dtype)
-        size = L.cl_int8_work_bytes(T, self.K)
+        size = L.cl_int8_work_bytes(T, self.N, self.K, 0)
         work = _s._empty(size, dtype=_s._torch.uint8, device=dev) if size else None
         st = L.cl_call(_FORWARD, _pack_forward(x.data_ptr(), _s._DT[x.dtype], row, T, self._clamp, *self._weights, yp, yd, yr,
                                                work.data_ptr() if size else 0, size, _s._stream(dev)))
@@ -175,8 +175,10 @@ class Int8Linear:
             rows = _s._empty(T, self._width, dtype=torch.int8, device=dev)
             rows[:, :self.K] = codes
             codes, row = rows, self._width
+        size = L.cl_int8_work_bytes(T, self.N, self.K, 1)
+        work = _s._empty(size, dtype=_s._torch.uint8, device=dev) if size else None
         st = L.cl_call(_LINEAR, _pack_linear(codes.data_ptr(), row, scale.data_ptr(), T, *self._weights, yp, yd, yr,
-                                             _s._stream(dev)))
+                                             work.data_ptr() if size else 0, size, _s._stream(dev)))
         if st:
             _s._check(st, "cl_int8_linear")
         return y

@@ -9,7 +9,7 @@
  * on the stream, nothing allocated, every entry recordable into a HIP graph, cl_dtype for element types, strides in
  * elements.  A call with no rows returns CL_OK and launches nothing.
  *
- * Codes lie in rows of `row` bytes, a multiple of 128 and at least K; a row's bytes from K to the next
+ * Codes lie in rows of `row` bytes, a multiple of 128, at least K and at most 2^23; a row's bytes from K to the next
  * multiple of 128 are readable, and zeros in weights.  Codes are 16-byte aligned.
  */
 #ifndef CL_INT8_H
@@ -42,20 +42,22 @@ cl_status cl_int8_quant(const void* x, int32_t dtype, int64_t x_row, int32_t row
  *   bias                 device, [N] fp32, or NULL
  *   y, y_dtype, y_row    device, [tokens, N], row stride y_row; the sum of products is rounded to fp32, then each product
  *                        with a scale and the sum with the bias, then the result to y's type
- * K <= 131071, so that no sum of products of two int8 passes 32 bits.
- * Errors: CL_EINVAL, CL_ESIZE, CL_EHIP.
+ *   work                 device, cl_int8_work_bytes(tokens, N, K, 1) bytes, 16-byte aligned (may be NULL where that is 0);
+ *                        it is this call's alone until the call has run
+ * K <= 131071, so that no sum of products of two int8 passes 32 bits; N <= 2^25.  A row's outputs do not depend on the other rows, nor
+ * on how many there are.
+ * Errors: CL_EINVAL, CL_ESIZE, CL_ENOMEM (work_bytes too small), CL_EHIP.
  */
+size_t cl_int8_work_bytes(int32_t tokens, int32_t N, int32_t K, int32_t quantised);
 cl_status cl_int8_linear(const int8_t* codes, int64_t row, const float* scale, int32_t tokens, const int8_t* w,
                          int64_t w_row, const float* w_scale, const float* bias, int32_t N, int32_t K, void* y,
-                         int32_t y_dtype, int64_t y_row, void* stream);
+                         int32_t y_dtype, int64_t y_row, void* work, size_t work_bytes, void* stream);
 
 /*
  * cl_int8_forward -- cl_int8_quant and cl_int8_linear in one call, and in one launch for a few tokens.
- *   work             device, cl_int8_work_bytes(tokens, K) bytes, 16-byte aligned (may be NULL where that is 0); it is this
- *                    call's alone until the call has run
- * Errors: as both; CL_ENOMEM (work_bytes too small).
+ *   work             device, cl_int8_work_bytes(tokens, N, K, 0) bytes, as for cl_int8_linear
+ * Errors: as both.
  */
-size_t cl_int8_work_bytes(int32_t tokens, int32_t K);
 cl_status cl_int8_forward(const void* x, int32_t dtype, int64_t x_row, int32_t tokens, float clamp, const int8_t* w,
                           int64_t w_row, const float* w_scale, const float* bias, int32_t N, int32_t K, void* y,
                           int32_t y_dtype, int64_t y_row, void* work, size_t work_bytes, void* stream);

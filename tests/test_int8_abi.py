@@ -32,8 +32,8 @@ def test_quant_refuses():
 def test_linear_refuses():
     L = cla.lib()
 
-    def linear(codes=P, row=128, scale=P, tokens=3, w=P, w_row=128, ws=P, bias=None, N=4, K=100, y=P, yd=0):
-        return L.cl_int8_linear(codes, row, scale, tokens, w, w_row, ws, bias, N, K, y, yd, 4, None)
+    def linear(codes=P, row=128, scale=P, tokens=3, w=P, w_row=128, ws=P, bias=None, N=4, K=100, y=P, yd=0, work=P, size=1 << 40):
+        return L.cl_int8_linear(codes, row, scale, tokens, w, w_row, ws, bias, N, K, y, yd, 4, work, size, None)
 
     def forward(x=P, dtype=0, tokens=3, clamp=0.0, w=P, w_row=128, ws=P, bias=None, N=4, K=100, y=P, yd=0, work=P, size=1 << 40):
         return L.cl_int8_forward(x, dtype, 100, tokens, clamp, w, w_row, ws, bias, N, K, y, yd, 4, work, size, None)
@@ -49,8 +49,14 @@ def test_linear_refuses():
         assert linear(**kw) == -1, kw
     for kw in (dict(x=None), dict(dtype=-1), dict(x=ODD), dict(clamp=-2.0)):
         assert forward(**kw) == -1, kw
-    assert L.cl_int8_work_bytes(0, 5) == 0 and L.cl_int8_work_bytes(5, 0) == 0 and L.cl_int8_work_bytes(5, 131072) == 0
-    need = L.cl_int8_work_bytes(4096, 100)
+    assert linear(row=(1 << 23) + 128) == -5 and linear(w_row=(1 << 23) + 128) == -5
+    for bad in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (5, 5, 131072)):
+        assert L.cl_int8_work_bytes(*bad, 0) == 0 and L.cl_int8_work_bytes(*bad, 1) == 0
+    need = L.cl_int8_work_bytes(4096, 4, 100, 0)
     assert need >= 4096 * 132
     assert forward(tokens=4096, size=need - 1) == -3
     assert forward(tokens=4096, work=None) == -1 and forward(tokens=4096, work=ctypes.c_void_p(264)) == -1
+    # few tokens of many channels: K is cut into parts
+    need = L.cl_int8_work_bytes(200, 1000, 100000, 1)
+    assert need >= 2 * 4 * 200 * 1000 and need < L.cl_int8_work_bytes(200, 1000, 100000, 0)
+    assert linear(tokens=200, N=1000, K=100000, row=100096, w_row=100096, size=need - 1) == -3
