@@ -19,26 +19,85 @@ inline int64_t padded(int64_t K) { return (K + 127) / 128 * 128; }
 __device__ __forceinline__ float clamped(float v, float clamp) { return clamp > 0.f && fabsf(v) > clamp ? copysignf(clamp, v) : v; }
 
 // ------------------------------------------------------------------- codes
-// A workgroup a row: its largest magnitude, as bits (a NaN is larger than any), then its codes.
-template <int IN>
-__global__ void __launch_bounds__(256) int8_quant_kernel(const typename Elem<IN>::raw* __restrict__ x, int64_t x_row, int64_t first, int K, int width,
-                                                         float clamp, int8_t* __restrict__ codes, int64_t row, float* __restrict__ scale) {
-  __shared__ uint32_t most[4];
+// Eight values of a row from k on, as they are quantised; zeros past its end.
+template <int IN, bool VEC>
+__device__ __forceinline__ void values8(const typename Elem<IN>::raw* x, int k, int K, float clamp, float (&v)[8]) {
+  if (VEC && k + 8 <= K) {
+    load8<IN>(x + k, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? Elem<IN>::up(x[k + i]) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = clamped(v[i], clamp);
+}
+
+__device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu; }
+
+// A row's scale and its inverse, from its largest magnitude as bits (those of a NaN or an infinity are larger than a number's).
+struct RowScale {
+  float scale, inverse;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t most) {
+  const float a = __builtin_bit_cast(float, most);
+  if (most >= 0x7f800000u) return {__builtin_nanf(""), 0.f};
+  if (a < kLeast) return {0.f, 0.f};
+  const float s = a * (1.f / 127.f);
+  return {s, 1.f / s};
+}
+
+// Eight codes in two words.  |v| (1 / s) passes 127 by its roundings only, which rint takes away; an inverse of 0 gives 0 whatever v is.
+__device__ __forceinline__ w2 codes8(const float (&v)[8], float inverse) {
+  w2 w = {0, 0};
+  if (inverse == 0.f) return w;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int)rintf(v[i] * inverse) & 255) << (8 * (i % 4));
+  return w;
+}
+
+// A workgroup a row, eight values to a thread at a time, the first HELD of them kept in registers between the two passes.
+// Bound by memory, few rows by the two trips to it.
+template <int IN, int THREADS, int HELD, bool VEC>
+__global__ void __launch_bounds__(THREADS) int8_quant_kernel(const typename Elem<IN>::raw* __restrict__ x, int64_t x_row, int64_t first, int K, int width,
+                                                             float clamp, int8_t* __restrict__ codes, int64_t row, float* __restrict__ scale) {
+  __shared__ uint32_t most[THREADS / 64];
   const int64_t t = first + blockIdx.x;
   x += t * x_row;
+  float held[HELD][8];
   uint32_t m = 0;
-  for (int k = threadIdx.x; k < K; k += 256) m = max(m, __builtin_bit_cast(uint32_t, fabsf(clamped(Elem<IN>::up(x[k]), clamp))));
+#pragma unroll
+  for (int c = 0; c < HELD; ++c) {
+    values8<IN, VEC>(x, 8 * (c * THREADS + threadIdx.x), K, clamp, held[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude(held[c][i]));
+  }
+  for (int k = 8 * (HELD * THREADS + threadIdx.x); k < K; k += 8 * THREADS) {
+    float v[8];
+    values8<IN, VEC>(x, k, K, clamp, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude(v[i]));
+  }
+#pragma unroll
   for (int d = 32; d; d /= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = max(max(most[0], most[1]), max(most[2], most[3]));
-  const float a = __builtin_bit_cast(float, m);
-  const bool fine = m < 0x7f800000u, any = fine && a >= kLeast;
-  const float s = any ? a * (1.f / 127.f) : fine ? 0.f : __builtin_nanf("");
-  const float r = any ? 1.f / s : 0.f;
-  if (threadIdx.x == 0) scale[t] = s;
-  for (int k = threadIdx.x; k < width; k += 256)
-    codes[t * row + k] = k < K && any ? (int8_t)fminf(fmaxf(rintf(clamped(Elem<IN>::up(x[k]), clamp) * r), -127.f), 127.f) : (int8_t)0;
+  if (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) m = max(m, most[w]);
+  }
+  const RowScale s = row_scale(m);
+  if (threadIdx.x == 0) scale[t] = s.scale;
+  w2* to = reinterpret_cast<w2*>(codes + t * row);
+#pragma unroll
+  for (int c = 0; c < HELD; ++c) {
+    const int k = 8 * (c * THREADS + threadIdx.x);
+    if (k < width) to[k / 8] = codes8(held[c], s.inverse);
+  }
+  for (int k = 8 * (HELD * THREADS + threadIdx.x); k < width; k += 8 * THREADS) {
+    float v[8];
+    values8<IN, VEC>(x, k, K, clamp, v);
+    to[k / 8] = codes8(v, s.inverse);
+  }
 }
 
 // ----------------------------------------------------------------- product
@@ -77,9 +136,12 @@ __device__ __forceinline__ float scaled(const Product& p, int sum, float s, int 
   return p.bias ? v + p.bias[n] : v;
 }
 
+// Waits until at most N loads are under way, those into LDS among them.
+template <int N>
 __device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt has six bits");
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | N >> 4 << 14);
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 __device__ __forceinline__ void wait_lds() {
@@ -95,11 +157,11 @@ __device__ __forceinline__ void meet() {
 
 // A tile of TW outputs by TT tokens, by GW x GT wavefronts of FW x FT blocks of 32 x 32 (v_mfma_i32_32x32x32_i8, weights as
 // the first operand, so that a lane has four outputs side by side of one token).  Steps of 128 k: the rows' 128 bytes come into LDS
-// directly, a step ahead, into the other of two buffers; a row's eight pieces of 16 bytes lie permuted by (row / 2) % 8, so that the 16
+// directly, DEPTH - 1 steps ahead, into a ring of DEPTH buffers; a row's eight pieces of 16 bytes lie permuted by (row / 2) % 8, so that the 16
 // lanes which LDS serves at once read all its banks.  A quarter step's operands are read between the products of the one before.  The
-// one barrier of a step stands before its last quarter, whose operands are in registers: behind it the other buffer has arrived
+// one barrier of a step stands before its last quarter, whose operands are in registers: behind it the next buffer has arrived
 // everywhere and this one is read by nobody.  Rows past the last give zeros (buffer loads with their bounds), and so do steps.
-template <int OUT, int TW, int TT, int GW, int GT>
+template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool ONCE>
 __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int n0, int first, int end, int part) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int WAVES = GW * GT, FW = TW / GW / 32, FT = TT / GT / 32, ROWS = TW + TT, STAGE = ROWS * 128;
@@ -123,7 +185,7 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
     for (int i = 0; i < LOADS; ++i) {
       auto to = (__attribute__((address_space(3))) void*)(lds + buf * STAGE + (i * WAVES + wave) * 1024);
       if (i * WAVES * 8 < TW)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(w, to, 16, at_row[i], step * 128, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w, to, 16, at_row[i], step * 128, 0, ONCE ? 2 : 0);
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(t, to, 16, at_row[i], step * 128, 0, 0);
     }
@@ -159,12 +221,13 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
       if (i < PRODUCTS) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
     }
   };
-  load(first, 0);
-  wait_loads();
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) load(first + d, d);
+  wait_loads<(DEPTH - 1) * LOADS>();
   meet();
-  load(first + 1, 1);
   read(0, 0, 0);
-  for (int at = first, buf = 0; at < end; ++at, buf ^= 1) {
+  for (int at = first, buf = 0; at < end; ++at) {
+    const int next = DEPTH == 2 ? buf ^ 1 : buf + 1 == DEPTH ? 0 : buf + 1;
     read(buf, 1, 1);
     multiply(0);
     mix(0);
@@ -175,15 +238,16 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
     multiply(0);
     mix(0);
     wait_lds();
-    wait_loads();
+    wait_loads<(DEPTH - 2) * LOADS>();
     meet();
-    load(at + 2, buf);
-    read(buf ^ 1, 0, 0);
+    load(at + DEPTH, buf);
+    read(next, 0, 0);
     multiply(1);
     mix(LOADS);
+    buf = next;
   }
   wait_lds();
-  wait_loads();
+  wait_loads<0>();
   meet();
   // Out through LDS, 32 tokens of a wavefront at a time, so that rows are written in pieces of 16 bytes.
   typedef typename Result<OUT>::raw raw;
@@ -192,7 +256,7 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
   const int nb = n0 + ww * FW * 32;
   raw* y = OUT == kSums ? reinterpret_cast<raw*>(p.sums) + (int64_t)part * p.tokens * p.pitch : static_cast<raw*>(p.y);
   const int64_t y_row = OUT == kSums ? p.pitch : p.y_row;
-  const bool whole = OUT == kSums || (reinterpret_cast<uintptr_t>(y) % 16 == 0 && y_row % PER == 0);
+  const bool whole = OUT == kSums || (reinterpret_cast<uintptr_t>(y) % 16 == 0 && y_row % PER == 0 && p.N % PER == 0);
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int tb = t0 + (wt * FT + j) * 32;
@@ -217,25 +281,17 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
       }
     wait_lds();
     __builtin_amdgcn_sched_barrier(0);
+    if (whole) {
 #pragma unroll
-    for (int k = 0; k < 32 / DOWN; ++k) {
-      const int down = k * DOWN + lane / ACROSS, across = lane % ACROSS * PER, t = tb + down, n = nb + across;
-      const w4 v = *reinterpret_cast<const w4*>(mine + down * PITCH + across * sizeof(raw));
-      if (t >= p.tokens || n >= p.N) continue;
-      raw* out = y + t * y_row + n;
-      if (whole && (OUT == kSums || n + PER <= p.N)) {
-        *reinterpret_cast<w4*>(out) = v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < PER; ++e)
-          if (n + e < p.N) {
-            const uint32_t word = v[sizeof(raw) == 4 ? e : e / 2];
-            if constexpr (sizeof(raw) == 4)
-              out[e] = __builtin_bit_cast(raw, word);
-            else
-              out[e] = (raw)(word >> (16 * (e % 2)));
-          }
+      for (int k = 0; k < 32 / DOWN; ++k) {
+        const int down = k * DOWN + lane / ACROSS, across = lane % ACROSS * PER, t = tb + down, n = nb + across;
+        if (t < p.tokens && n < p.N)
+          *reinterpret_cast<w4*>(y + t * y_row + n) = *reinterpret_cast<const w4*>(mine + down * PITCH + across * sizeof(raw));
       }
+    } else {  // an element to a lane, so that a wavefront still writes one run
+      for (int down = 0; down < min(32, p.tokens - tb); ++down)
+        for (int n = lane; n < min(FW * 32, p.N - nb); n += 64)
+          y[(tb + down) * y_row + nb + n] = *reinterpret_cast<const raw*>(mine + down * PITCH + n * sizeof(raw));
     }
     wait_lds();
     __builtin_amdgcn_sched_barrier(0);
@@ -253,13 +309,13 @@ __device__ __forceinline__ int of_xcd(int id, int n) {
   const int xcd = id & 7, each = n >> 3, extra = n & 7;
   return xcd * each + min(xcd, extra) + (id >> 3);
 }
-// Two buffers of a step's rows, or 32 rows of each wavefront's outputs.
-constexpr int lds_bytes(int tw, int tt, int waves, int out) {
-  return 2 * (tw + tt) * 128 > waves * 32 * (out + 16) ? 2 * (tw + tt) * 128 : waves * 32 * (out + 16);
+// The ring of a step's rows, or 32 rows of each wavefront's outputs.
+constexpr int lds_bytes(int rows, int depth, int waves, int out) {
+  return depth * rows * 128 > waves * 32 * (out + 16) ? depth * rows * 128 : waves * 32 * (out + 16);
 }
-template <int OUT, int TW, int TT, int GW, int GT, bool HALVES>
+template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool HALVES, bool ONCE>
 __global__ void __launch_bounds__(64 * GW * GT, 2) int8_tile_kernel(Product p, Tiles g) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[lds_bytes(TW, TT, GW * GT, TW / GW * (int)sizeof(typename Result<OUT>::raw))];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[lds_bytes(TW + TT, DEPTH, GW * GT, TW / GW * (int)sizeof(typename Result<OUT>::raw))];
   const bool half = HALVES && (int)blockIdx.x >= g.full;
   const int unit = half ? of_xcd(blockIdx.x - g.full, gridDim.x - g.full) : of_xcd(blockIdx.x, HALVES ? g.full : gridDim.x);
   const int tiles = g.t * g.w, at = half ? g.full + (unit >> 1) : unit, part = at / tiles, number = at % tiles;
@@ -269,15 +325,15 @@ __global__ void __launch_bounds__(64 * GW * GT, 2) int8_tile_kernel(Product p, T
   if constexpr (HALVES) {
     if (half) {
       const int t = t0 + (unit & 1) * (TT / 2);
-      if (t < p.tokens) tile<OUT, TW, TT / 2, GW, GT>(p, lds, t, n0, first, end, part);
+      if (t < p.tokens) tile<OUT, TW, TT / 2, GW, GT, DEPTH, ONCE>(p, lds, t, n0, first, end, part);
       return;
     }
   }
-  tile<OUT, TW, TT, GW, GT>(p, lds, t0, n0, first, end, part);
+  tile<OUT, TW, TT, GW, GT, DEPTH, ONCE>(p, lds, t0, n0, first, end, part);
 }
 
 // Sums of parts of K to outputs, four to a thread.
-template <int OUT>
+template <int OUT, bool WHOLE>
 __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, int64_t first) {
   const int64_t at = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int across = p.pitch / 4, n = 4 * (int)(at % across);
@@ -287,80 +343,85 @@ __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, in
   for (int k = 0; k < parts; ++k) sum += *reinterpret_cast<const i4*>(p.sums + (k * (int64_t)p.tokens + t) * p.pitch + n);
   const float s = p.scale[t];
   typename Elem<OUT>::raw* y = static_cast<typename Elem<OUT>::raw*>(p.y) + t * p.y_row + n;
+  float v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (n + e < p.N) y[e] = Elem<OUT>::down(scaled(p, sum[e], s, n + e));
+  for (int e = 0; e < 4; ++e) v[e] = scaled(p, sum[e], s, min(n + e, p.N - 1));
+  if constexpr (WHOLE) {
+    if constexpr (OUT == CL_F32)
+      *reinterpret_cast<v4*>(y) = v4{v[0], v[1], v[2], v[3]};
+    else
+      *reinterpret_cast<w2*>(y) = w2{down2<OUT>(v[0], v[1]), down2<OUT>(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < p.N) y[e] = Elem<OUT>::down(v[e]);
+  }
 }
 
 // ------------------------------------------------------------- few tokens
-// Up to 64 tokens: the weights are read once and nothing is shared but tokens, so operands come from memory into registers as they
-// are (v_mfma_i32_16x16x64_i8; a lane has 32 bytes of a row in a step of 128 k, the same ones in both operands).  A workgroup has
-// 16 FW outputs, its wavefronts take the steps in turn, and the sums meet in LDS.  AHEAD steps are asked for while as many are multiplied.
-template <int OUT, int FW, int FT, int WAVES>
+// Up to 16 tokens: the weights are read once.  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
+// ring of DEPTH buffers in LDS to itself, so that they wait for their own loads only, and their sums meet in LDS at the end
+// (v_mfma_i32_16x16x64_i8, weights as the first operand).  Rows lie as in a tile; TR (8 or 16) token rows come with the weights.
+template <int OUT, int WAVES, int DEPTH, int TR>
 __global__ void __launch_bounds__(64 * WAVES) int8_stream_kernel(Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int AHEAD = FW * FT >= 8 ? 1 : 2;
-  __shared__ i4 sums[WAVES][FW][FT][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 16 * FW;
-  const int r = lane & 15, at = lane >> 4;
+  constexpr int LOADS = (16 + TR) / 8, STAGE = (16 + TR) * 128;
+  __shared__ __attribute__((aligned(128))) uint8_t ring[WAVES][DEPTH][STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 16;
   const int8_t* w_base = p.w + (int64_t)n0 * p.w_row;
-  const uint32_t w_bytes = (uint32_t)(min(16 * FW, p.N - n0) * p.w_row), t_bytes = (uint32_t)(p.tokens * p.row);
-  uint32_t w_at[FW], t_at[FT];
+  const uint32_t w_bytes = (uint32_t)(min(16, p.N - n0) * p.w_row), t_bytes = (uint32_t)(p.tokens * p.row);
+  uint32_t at_row[LOADS];
 #pragma unroll
-  for (int i = 0; i < FW; ++i) w_at[i] = (uint32_t)((16 * i + r) * p.w_row) + at * 32;
+  for (int i = 0; i < LOADS; ++i) {
+    const int r = i * 8 + (lane >> 3), piece = (lane & 7) ^ ((r >> 1) & 7);
+    at_row[i] = (i < 2 ? (uint32_t)(r * p.w_row) : (uint32_t)((r - 16) * p.row)) + piece * 16;
+  }
+  const auto load = [&](int step, int buf) {
+    const bool any = step < p.steps;
+    const auto w = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(w_base), 0, any ? w_bytes : 0, 0x00020000);
+    const auto t = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p.codes), 0, any ? t_bytes : 0, 0x00020000);
 #pragma unroll
-  for (int j = 0; j < FT; ++j) t_at[j] = (uint32_t)((16 * j + r) * p.row) + at * 32;
-  i4 fw[2][AHEAD][FW][2], ft[2][AHEAD][FT][2];
-  i4 acc[FW][FT] = {};
-  const auto load = [&](int step, int to) {
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int k = step + a * WAVES;
-      const auto w = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(w_base), 0, k < p.steps ? w_bytes : 0, 0x00020000);
-      const auto t = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p.codes), 0, k < p.steps ? t_bytes : 0, 0x00020000);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < FW; ++i) fw[to][a][i][h] = __builtin_amdgcn_raw_buffer_load_b128(w, w_at[i] + 16 * h, k * 128, 2);
-#pragma unroll
-        for (int j = 0; j < FT; ++j) ft[to][a][j][h] = __builtin_amdgcn_raw_buffer_load_b128(t, t_at[j] + 16 * h, k * 128, 0);
-      }
+    for (int i = 0; i < LOADS; ++i) {
+      auto to = (__attribute__((address_space(3))) void*)(ring[wave][buf] + i * 1024);
+      if (i < 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(w, to, 16, at_row[i], step * 128, 0, 2);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(t, to, 16, at_row[i], step * 128, 0, 0);
     }
   };
-  const auto multiply = [&](int of) {
+  const int r = lane & 15, q = lane >> 4, tr = 16 + (TR == 16 ? r : r & 7);
+  uint32_t w_at[2], t_at[2];
 #pragma unroll
-    for (int a = 0; a < AHEAD; ++a)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < FW; ++i)
-#pragma unroll
-          for (int j = 0; j < FT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[of][a][i][h], ft[of][a][j][h], acc[i][j], 0, 0, 0);
-  };
-  load(wave, 0);
-  for (int step = wave; step < p.steps; step += 2 * AHEAD * WAVES) {
-    load(step + AHEAD * WAVES, 1);
-    multiply(0);
-    load(step + 2 * AHEAD * WAVES, 0);
-    multiply(1);
+  for (int h = 0; h < 2; ++h) {
+    w_at[h] = r * 128 + ((q + 4 * h) ^ ((r >> 1) & 7)) * 16;
+    t_at[h] = tr * 128 + ((q + 4 * h) ^ ((tr >> 1) & 7)) * 16;
   }
+  i4 acc[2] = {};
 #pragma unroll
-  for (int i = 0; i < FW; ++i)
+  for (int d = 0; d < DEPTH; ++d) load(wave + d * WAVES, d);
+  for (int step = wave, buf = 0; step < p.steps; step += WAVES) {
+    wait_loads<(DEPTH - 1) * LOADS>();
+    const uint8_t* at = ring[wave][buf];
+    i4 fw[2], ft[2];
 #pragma unroll
-    for (int j = 0; j < FT; ++j) sums[wave][i][j][lane] = acc[i][j];
+    for (int h = 0; h < 2; ++h) fw[h] = *reinterpret_cast<const i4*>(at + w_at[h]), ft[h] = *reinterpret_cast<const i4*>(at + t_at[h]);
+    wait_lds();
+    load(step + DEPTH * WAVES, buf);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) acc[h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h], ft[h], acc[h], 0, 0, 0);
+    buf = buf + 1 == DEPTH ? 0 : buf + 1;
+  }
+  wait_loads<0>();
+  *reinterpret_cast<i4*>(ring[wave][0] + lane * 16) = acc[0] + acc[1];
   __syncthreads();
-  // a lane of the sums has outputs 4 (l / 16) to + 3 of token l % 16
-  for (int k = threadIdx.x; k < FW * FT * 64; k += 64 * WAVES) {
-    const int l = k & 63, i = (k >> 6) % FW, j = (k >> 6) / FW, t = 16 * j + (l & 15), n = n0 + 16 * i + 4 * (l >> 4);
-    i4 sum = sums[0][i][j][l];
+  // a lane of the sums has outputs 4 (lane / 16) to + 3 of token lane % 16; a thread takes one
+  if (threadIdx.x < 256) {
+    const int t = threadIdx.x >> 4, n = threadIdx.x & 15;
+    int sum = 0;
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += sums[w][i][j][l];
-    if (t >= p.tokens) continue;
-    const float s = p.scale[t];
-    typename Elem<OUT>::raw* y = static_cast<typename Elem<OUT>::raw*>(p.y) + t * p.y_row + n;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < p.N) y[e] = Elem<OUT>::down(scaled(p, sum[e], s, n + e));
+    for (int w = 0; w < WAVES; ++w) sum += *reinterpret_cast<const int*>(ring[w][0] + ((n >> 2) * 16 + t) * 16 + (n & 3) * 4);
+    if (t < p.tokens && n0 + n < p.N)
+      static_cast<typename Elem<OUT>::raw*>(p.y)[t * p.y_row + n0 + n] = Elem<OUT>::down(scaled(p, sum, p.scale[t], n0 + n));
   }
 #endif
 }
@@ -411,12 +472,27 @@ cl_status check_values(const void* x, int dtype, int K, float clamp) {
   return CL_OK;
 }
 
+template <int IN, int THREADS, int HELD>
+void launch_quant(const void* x, int64_t x_row, int rows, int K, float clamp, int8_t* codes, int64_t row, float* scale, hipStream_t s) {
+  const auto kernel = heads_aligned(x, IN, x_row, 0) ? int8_quant_kernel<IN, THREADS, HELD, true> : int8_quant_kernel<IN, THREADS, HELD, false>;
+  in_pieces(rows, THREADS, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)count), dim3(THREADS), 0, s, static_cast<const typename Elem<IN>::raw*>(x), x_row, first, K,
+                       (int)padded(K), clamp, codes, row, scale);
+  });
+}
+
+// A row of up to 8192 values is 256 threads' registers, or 1024 threads' where rows are few and the trips to memory count; longer
+// ones are 1024 threads', up to 32768.
 template <int IN>
 void launch_quant(const void* x, int64_t x_row, int rows, int K, float clamp, int8_t* codes, int64_t row, float* scale, hipStream_t s) {
-  in_pieces(rows, 256, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL((int8_quant_kernel<IN>), dim3((unsigned)count), dim3(256), 0, s, static_cast<const typename Elem<IN>::raw*>(x), x_row, first,
-                       K, (int)padded(K), clamp, codes, row, scale);
-  });
+  if (K <= 2048)
+    launch_quant<IN, 256, 1>(x, x_row, rows, K, clamp, codes, row, scale, s);
+  else if (K <= 8192 && rows < 512)
+    launch_quant<IN, 1024, 1>(x, x_row, rows, K, clamp, codes, row, scale, s);
+  else if (K <= 8192)
+    launch_quant<IN, 256, 4>(x, x_row, rows, K, clamp, codes, row, scale, s);
+  else
+    launch_quant<IN, 1024, 4>(x, x_row, rows, K, clamp, codes, row, scale, s);
 }
 
 void launch_quant(const void* x, int dtype, int64_t x_row, int rows, int K, float clamp, int8_t* codes, int64_t row, float* scale, hipStream_t s) {
@@ -430,87 +506,106 @@ void launch_quant(const void* x, int dtype, int64_t x_row, int rows, int K, floa
 
 // ------------------------------------------------------------------- plan
 constexpr int kCus = 256;
-constexpr int kFewTokens = 64;
+constexpr int kStreamed = 16;  // tokens up to which int8_stream_kernel takes a product
+constexpr int kMostParts = 16;
 
 // How a product is cut: the tile, parts of K.
 struct Plan {
   int shape = 0, parts = 1;
 };
+
+// Tiles, and what they were measured to cost: the microseconds that a step of 128 k takes a CU for each tile that it has, and how
+// many of them run at once.  Few large tiles wait for their loads (256 x 128 with three buffers 1.19 us a step, with two 1.25 where the tile of
+// twice the size takes 1.72); small ones run side by side and fill in for each other, but read more for what they multiply.
 struct Shape {
-  int tw, tt;
-  double step, twice;  // microseconds of a step of 128 k with one tile to each CU, and with two
+  int tw, tt, together;
+  float step;
 };
-constexpr Shape kShapes[] = {{256, 256, 1.85, 0}, {256, 192, 1.50, 0}, {256, 128, 1.05, 0}, {128, 128, 0.70, 1.10}};
+constexpr Shape kShapes[] = {{256, 256, 1, 1.72f}, {256, 192, 1, 1.45f}, {256, 128, 1, 1.19f}, {128, 128, 1, 0.54f},
+                             {128, 64, 2, 0.46f},  {64, 64, 2, 0.265f},  {64, 32, 3, 0.235f}};
+constexpr int kShapeCount = sizeof kShapes / sizeof kShapes[0], kHalf = 2;
 
-int tiles_of(const Shape& s, int tokens, int N) { return ((tokens + s.tt - 1) / s.tt) * ((N + s.tw - 1) / s.tw); }
+int64_t tiles_of(const Shape& s, int tokens, int N) { return (int64_t)((tokens + s.tt - 1) / s.tt) * ((N + s.tw - 1) / s.tw); }
 
+// Half of the last round's tiles or fewer: each is cut in two, so that the round takes half the time.
+bool halved(int64_t tiles) { return tiles % kCus && tiles % kCus <= kCus / 2; }
+
+// The cheapest of the tiles and parts of K by those costs: steps x tiles of the busiest CU, 3.5 us to fill and to empty each, at least the
+// time to read the weights (8 bytes a picosecond is more than memory gives: it ranks the small products), and for parts 4 us and the sums
+// written and read at 4.2 bytes a picosecond.  Over 100 products of 24 to 4096 tokens and 1000 x 1000 to 8192 x 28672 weights the choice
+// is 2 % slower than the best of all in the mean, 25 % at worst; 256 x 256 tiles alone would be up to eight times slower.
 Plan plan_product(int tokens, int N, int K) {
-  const int steps = (int)(padded(K) / 128);
   Plan best;
-  if ((int64_t)tokens * N > (1 << 28)) return best;  // 4096 tiles: no parts, and the largest is the best
-  double least = 1e30;
-  for (int shape = 0; shape < 4; ++shape)
-    for (int parts = 1; parts <= 16 && parts <= (steps + 7) / 8; ++parts) {
-      const Shape& s = kShapes[shape];
-      const int64_t n = (int64_t)tiles_of(s, tokens, N) * parts;
-      const int64_t rounds = n / kCus, rest = n % kCus;
-      double unit;  // in steps
-      if (s.twice)
-        unit = (n / (2 * kCus)) * s.twice + (n % (2 * kCus) > kCus ? s.twice : n % (2 * kCus) ? s.step : 0);
-      else
-        unit = rounds * s.step + (rest == 0 ? 0 : shape == 0 && parts == 1 && rest <= kCus / 2 ? kShapes[2].step : s.step);
-      const double overhead = 6.0 * (double)((n + kCus - 1) / kCus);
-      double t = unit * ((steps + parts - 1) / parts) + overhead;
-      const double sums = 4.0 * tokens * N * parts;
-      if (parts > 1) t += 4.0 + 2 * sums / 6e6;
-      if (parts > 1 && sums > 268435456.0) continue;
+  if (tiles_of(kShapes[0], tokens, N) > 4 * kCus) return best;
+  const int steps = (int)(padded(K) / 128);
+  float least = 1e30f;
+  for (int shape = 0; shape < kShapeCount; ++shape) {
+    const Shape& s = kShapes[shape];
+    const int64_t tiles = tiles_of(s, tokens, N);
+    for (int parts = 1; parts <= kMostParts && parts <= (steps + 3) / 4; ++parts) {
+      const int64_t n = tiles * parts;
+      if (parts > 1 && n > 4 * kCus) break;
+      const int each = (steps + parts - 1) / parts;
+      const bool half = shape == 0 && halved(n);
+      const int64_t whole = half ? n / kCus : (n + kCus - 1) / kCus;
+      float t = each * (whole * s.step + (half ? kShapes[kHalf].step : 0)) + 3.5f * ((whole + s.together - 1) / s.together + half);
+      t = std::max(t, (float)N * K / 8e6f);
+      if (parts > 1) t += 4.f + 4.f * tokens * N * parts / 4.2e6f;
       if (t < least) least = t, best = Plan{shape, parts};
     }
+  }
   return best;
 }
 
 size_t sums_bytes(int tokens, int N, int K) {
-  if (tokens <= kFewTokens) return 0;
+  if (tokens <= kStreamed) return 0;
   const Plan p = plan_product(tokens, N, K);
   return p.parts > 1 ? (size_t)4 * p.parts * tokens * ((N + 3) / 4 * 4) : 0;
 }
 
-template <int OUT, int TW, int TT, int GW, int GT, bool HALVES>
+template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool HALVES, bool ONCE>
 void launch_tiles(const Product& p, int parts, hipStream_t s) {
   Tiles g{(p.tokens + TT - 1) / TT, (p.N + TW - 1) / TW, parts, 0};
   const int n = g.t * g.w * parts, rest = n % kCus;
   g.full = n;
   int blocks = n;
-  if (HALVES && rest && rest <= kCus / 2) g.full = n - rest, blocks = g.full + 2 * rest;
-  const auto kernel = int8_tile_kernel<OUT, TW, TT, GW, GT, HALVES>;
+  if (HALVES && halved(n)) g.full = n - rest, blocks = g.full + 2 * rest;
+  const auto kernel = int8_tile_kernel<OUT, TW, TT, GW, GT, DEPTH, HALVES, ONCE>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(64 * GW * GT), 0, s, p, g);
 }
 
 template <int OUT>
 void launch_shape(const Product& p, const Plan& plan, hipStream_t s) {
   switch (plan.shape) {
-    case 0: return launch_tiles<OUT, 256, 256, 4, 2, true>(p, plan.parts, s);
-    case 1: return launch_tiles<OUT, 256, 192, 4, 2, false>(p, plan.parts, s);
-    case 2: return launch_tiles<OUT, 256, 128, 4, 2, false>(p, plan.parts, s);
-    default: return launch_tiles<OUT, 128, 128, 4, 2, false>(p, plan.parts, s);
+    case 0: return launch_tiles<OUT, 256, 256, 4, 2, 2, true, false>(p, plan.parts, s);
+    case 1: return launch_tiles<OUT, 256, 192, 4, 2, 2, false, false>(p, plan.parts, s);
+    case 2: return launch_tiles<OUT, 256, 128, 4, 2, 3, false, false>(p, plan.parts, s);
+    case 3: return launch_tiles<OUT, 128, 128, 4, 2, 4, false, false>(p, plan.parts, s);
+    case 4: return launch_tiles<OUT, 128, 64, 4, 2, 3, false, true>(p, plan.parts, s);
+    case 5: return launch_tiles<OUT, 64, 64, 2, 2, 4, false, true>(p, plan.parts, s);
+    default: return launch_tiles<OUT, 64, 32, 2, 1, 4, false, true>(p, plan.parts, s);
   }
 }
 
-template <int OUT, int FW, int FT>
+template <int OUT, int WAVES, int DEPTH, int TR>
 void launch_stream(const Product& p, hipStream_t s) {
-  hipLaunchKernelGGL((int8_stream_kernel<OUT, FW, FT, 8>), dim3((unsigned)((p.N + 16 * FW - 1) / (16 * FW))), dim3(512), 0, s, p);
+  static_assert(WAVES >= 4, "256 threads write a workgroup's outputs");
+  hipLaunchKernelGGL((int8_stream_kernel<OUT, WAVES, DEPTH, TR>), dim3((unsigned)((p.N + 15) / 16)), dim3(64 * WAVES), 0, s, p);
 }
 
 template <int OUT>
 void launch_piece(const Product& p, int K, hipStream_t s) {
-  if (p.tokens <= 16) return launch_stream<OUT, 1, 1>(p, s);
-  if (p.tokens <= 32) return launch_stream<OUT, 2, 2>(p, s);
-  if (p.tokens <= kFewTokens) return launch_stream<OUT, 2, 4>(p, s);
+  // eight wavefronts with three buffers: one token of 8192 x 10240 15.4 us, four with three or four 16.5, sixteen 18; with 16 token rows
+  // two buffers (16 tokens of 8192 x 28672 40.9 us, three 48)
+  if (p.tokens <= 8) return launch_stream<OUT, 8, 3, 8>(p, s);
+  if (p.tokens <= kStreamed) return launch_stream<OUT, 8, 2, 16>(p, s);
   const Plan plan = plan_product(p.tokens, p.N, K);
   if (plan.parts == 1) return launch_shape<OUT>(p, plan, s);
   launch_shape<kSums>(p, plan, s);
+  const bool whole = p.N % 4 == 0 && p.y_row % 4 == 0 && aligned_to(p.y, 4 * elem_size(OUT));
+  const auto join = whole ? int8_join_kernel<OUT, true> : int8_join_kernel<OUT, false>;
   in_pieces((int64_t)p.tokens * (p.pitch / 4), 1, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL((int8_join_kernel<OUT>), dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, plan.parts, first);
+    hipLaunchKernelGGL(join, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, plan.parts, first);
   });
 }
 
