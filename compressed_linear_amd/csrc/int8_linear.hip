@@ -359,13 +359,13 @@ __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, in
 }
 
 // ------------------------------------------------------------- few tokens
-// Up to 16 tokens: the weights are read once.  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
+// Few tokens: the weights are read once.  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
 // ring of DEPTH buffers in LDS to itself, so that they wait for their own loads only, and their sums meet in LDS at the end
-// (v_mfma_i32_16x16x64_i8, weights as the first operand).  Rows lie as in a tile; TR (8 or 16) token rows come with the weights.
+// (v_mfma_i32_16x16x64_i8, weights as the first operand).  Rows lie as in a tile; TR (8, or a multiple of 16) token rows come with the weights.
 template <int OUT, int WAVES, int DEPTH, int TR>
 __global__ void __launch_bounds__(64 * WAVES) int8_stream_kernel(Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int LOADS = (16 + TR) / 8, STAGE = (16 + TR) * 128;
+  constexpr int LOADS = (16 + TR) / 8, STAGE = (16 + TR) * 128, FT = (TR + 15) / 16;
   __shared__ __attribute__((aligned(128))) uint8_t ring[WAVES][DEPTH][STAGE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = blockIdx.x * 16;
   const int8_t* w_base = p.w + (int64_t)n0 * p.w_row;
@@ -389,39 +389,46 @@ __global__ void __launch_bounds__(64 * WAVES) int8_stream_kernel(Product p) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(t, to, 16, at_row[i], step * 128, 0, 0);
     }
   };
-  const int r = lane & 15, q = lane >> 4, tr = 16 + (TR == 16 ? r : r & 7);
+  const int r = lane & 15, q = lane >> 4, tr = 16 + (TR == 8 ? r & 7 : r);
   uint32_t w_at[2], t_at[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     w_at[h] = r * 128 + ((q + 4 * h) ^ ((r >> 1) & 7)) * 16;
     t_at[h] = tr * 128 + ((q + 4 * h) ^ ((tr >> 1) & 7)) * 16;
   }
-  i4 acc[2] = {};
+  i4 acc[2][FT] = {};
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) load(wave + d * WAVES, d);
   for (int step = wave, buf = 0; step < p.steps; step += WAVES) {
     wait_loads<(DEPTH - 1) * LOADS>();
     const uint8_t* at = ring[wave][buf];
-    i4 fw[2], ft[2];
+    i4 fw[2], ft[2][FT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) fw[h] = *reinterpret_cast<const i4*>(at + w_at[h]), ft[h] = *reinterpret_cast<const i4*>(at + t_at[h]);
+    for (int h = 0; h < 2; ++h) {
+      fw[h] = *reinterpret_cast<const i4*>(at + w_at[h]);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) ft[h][j] = *reinterpret_cast<const i4*>(at + t_at[h] + j * 2048);
+    }
     wait_lds();
     load(step + DEPTH * WAVES, buf);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) acc[h] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h], ft[h], acc[h], 0, 0, 0);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < FT; ++j) acc[h][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[h], ft[h][j], acc[h][j], 0, 0, 0);
     buf = buf + 1 == DEPTH ? 0 : buf + 1;
   }
   wait_loads<0>();
-  *reinterpret_cast<i4*>(ring[wave][0] + lane * 16) = acc[0] + acc[1];
+#pragma unroll
+  for (int j = 0; j < FT; ++j) *reinterpret_cast<i4*>(ring[wave][0] + j * 1024 + lane * 16) = acc[0][j] + acc[1][j];
   __syncthreads();
-  // a lane of the sums has outputs 4 (lane / 16) to + 3 of token lane % 16; a thread takes one
-  if (threadIdx.x < 256) {
-    const int t = threadIdx.x >> 4, n = threadIdx.x & 15;
+  // a lane of a block's sums has outputs 4 (lane / 16) to + 3 of token lane % 16; a thread takes one at a time
+  for (int k = threadIdx.x; k < FT * 256; k += 64 * WAVES) {
+    const int j = k >> 8, t = k >> 4 & 15, n = k & 15;
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += *reinterpret_cast<const int*>(ring[w][0] + ((n >> 2) * 16 + t) * 16 + (n & 3) * 4);
-    if (t < p.tokens && n0 + n < p.N)
-      static_cast<typename Elem<OUT>::raw*>(p.y)[t * p.y_row + n0 + n] = Elem<OUT>::down(scaled(p, sum, p.scale[t], n0 + n));
+    for (int w = 0; w < WAVES; ++w) sum += *reinterpret_cast<const int*>(ring[w][0] + j * 1024 + ((n >> 2) * 16 + t) * 16 + (n & 3) * 4);
+    if (16 * j + t < p.tokens && n0 + n < p.N)
+      static_cast<typename Elem<OUT>::raw*>(p.y)[(16 * j + t) * p.y_row + n0 + n] = Elem<OUT>::down(scaled(p, sum, p.scale[16 * j + t], n0 + n));
   }
 #endif
 }
@@ -506,7 +513,10 @@ void launch_quant(const void* x, int dtype, int64_t x_row, int rows, int K, floa
 
 // ------------------------------------------------------------------- plan
 constexpr int kCus = 256;
-constexpr int kStreamed = 16;  // tokens up to which int8_stream_kernel takes a product
+// What int8_stream_kernel takes: up to 16 tokens, and up to 64 with few weights, where reading the tokens once for every 16 outputs costs
+// less than the start of tiles (32 tokens of 4096 x 4096 6.7 us, as tiles 10; 64 8.8 and 10.7; of 4096 x 11008 14.9 and 12.7, of
+// 11008 x 4096 64 18.4 and 16.3).
+bool streamed(int tokens, int N, int K) { return tokens <= 16 || (tokens <= 64 && (int64_t)N * K <= 1 << 25); }
 constexpr int kMostParts = 16;
 
 // How a product is cut: the tile, parts of K.
@@ -558,7 +568,7 @@ Plan plan_product(int tokens, int N, int K) {
 }
 
 size_t sums_bytes(int tokens, int N, int K) {
-  if (tokens <= kStreamed) return 0;
+  if (streamed(tokens, N, K)) return 0;
   const Plan p = plan_product(tokens, N, K);
   return p.parts > 1 ? (size_t)4 * p.parts * tokens * ((N + 3) / 4 * 4) : 0;
 }
@@ -589,16 +599,16 @@ void launch_shape(const Product& p, const Plan& plan, hipStream_t s) {
 
 template <int OUT, int WAVES, int DEPTH, int TR>
 void launch_stream(const Product& p, hipStream_t s) {
-  static_assert(WAVES >= 4, "256 threads write a workgroup's outputs");
   hipLaunchKernelGGL((int8_stream_kernel<OUT, WAVES, DEPTH, TR>), dim3((unsigned)((p.N + 15) / 16)), dim3(64 * WAVES), 0, s, p);
 }
 
 template <int OUT>
 void launch_piece(const Product& p, int K, hipStream_t s) {
-  // eight wavefronts with three buffers: one token of 8192 x 10240 15.4 us, four with three or four 16.5, sixteen 18; with 16 token rows
-  // two buffers (16 tokens of 8192 x 28672 40.9 us, three 48)
+  // eight wavefronts with three buffers: one token of 8192 x 10240 15.4 us, four with three or four 16.5, sixteen 18; with more token rows
+  // two buffers (16 tokens of 8192 x 28672 40.9 us, three 48) and four wavefronts (32 tokens of 4096 x 11008 14.9, eight 17.4)
   if (p.tokens <= 8) return launch_stream<OUT, 8, 3, 8>(p, s);
-  if (p.tokens <= kStreamed) return launch_stream<OUT, 8, 2, 16>(p, s);
+  if (p.tokens <= 16) return launch_stream<OUT, 8, 2, 16>(p, s);
+  if (streamed(p.tokens, p.N, K)) return p.tokens <= 32 ? launch_stream<OUT, 4, 2, 32>(p, s) : launch_stream<OUT, 4, 2, 64>(p, s);
   const Plan plan = plan_product(p.tokens, p.N, K);
   if (plan.parts == 1) return launch_shape<OUT>(p, plan, s);
   launch_shape<kSums>(p, plan, s);
