@@ -19,11 +19,15 @@ inline int64_t padded(int64_t K) { return (K + 127) / 128 * 128; }
 __device__ __forceinline__ float clamped(float v, float clamp) { return clamp > 0.f && fabsf(v) > clamp ? copysignf(clamp, v) : v; }
 
 // ------------------------------------------------------------------- codes
-// Eight values of a row from k on, as they are quantised; zeros past its end.
-template <int IN, bool VEC>
+// Eight values of a row from k on, as they are quantised; zeros past its end.  Rows may lie at any multiple of an element: the hardware
+// takes loads of 16 bytes there.
+template <int IN>
 __device__ __forceinline__ void values8(const typename Elem<IN>::raw* x, int k, int K, float clamp, float (&v)[8]) {
-  if (VEC && k + 8 <= K) {
-    load8<IN>(x + k, v);
+  if (k + 8 <= K) {
+    typename Elem<IN>::raw some[8];
+    __builtin_memcpy(some, x + k, sizeof some);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = Elem<IN>::up(some[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = k + i < K ? Elem<IN>::up(x[k + i]) : 0.f;
@@ -57,7 +61,7 @@ __device__ __forceinline__ w2 codes8(const float (&v)[8], float inverse) {
 
 // A workgroup a row, eight values to a thread at a time, the first HELD of them kept in registers between the two passes.
 // Bound by memory, few rows by the two trips to it.
-template <int IN, int THREADS, int HELD, bool VEC>
+template <int IN, int THREADS, int HELD>
 __global__ void __launch_bounds__(THREADS) int8_quant_kernel(const typename Elem<IN>::raw* __restrict__ x, int64_t x_row, int64_t first, int K, int width,
                                                              float clamp, int8_t* __restrict__ codes, int64_t row, float* __restrict__ scale) {
   __shared__ uint32_t most[THREADS / 64];
@@ -67,13 +71,13 @@ __global__ void __launch_bounds__(THREADS) int8_quant_kernel(const typename Elem
   uint32_t m = 0;
 #pragma unroll
   for (int c = 0; c < HELD; ++c) {
-    values8<IN, VEC>(x, 8 * (c * THREADS + threadIdx.x), K, clamp, held[c]);
+    values8<IN>(x, 8 * (c * THREADS + threadIdx.x), K, clamp, held[c]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, magnitude(held[c][i]));
   }
   for (int k = 8 * (HELD * THREADS + threadIdx.x); k < K; k += 8 * THREADS) {
     float v[8];
-    values8<IN, VEC>(x, k, K, clamp, v);
+    values8<IN>(x, k, K, clamp, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, magnitude(v[i]));
   }
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(THREADS) int8_quant_kernel(const typename Elem
   }
   for (int k = 8 * (HELD * THREADS + threadIdx.x); k < width; k += 8 * THREADS) {
     float v[8];
-    values8<IN, VEC>(x, k, K, clamp, v);
+    values8<IN>(x, k, K, clamp, v);
     to[k / 8] = codes8(v, s.inverse);
   }
 }
@@ -256,7 +260,6 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
   const int nb = n0 + ww * FW * 32;
   raw* y = OUT == kSums ? reinterpret_cast<raw*>(p.sums) + (int64_t)part * p.tokens * p.pitch : static_cast<raw*>(p.y);
   const int64_t y_row = OUT == kSums ? p.pitch : p.y_row;
-  const bool whole = OUT == kSums || (reinterpret_cast<uintptr_t>(y) % 16 == 0 && y_row % PER == 0 && p.N % PER == 0);
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int tb = t0 + (wt * FT + j) * 32;
@@ -281,17 +284,19 @@ __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int
       }
     wait_lds();
     __builtin_amdgcn_sched_barrier(0);
-    if (whole) {
 #pragma unroll
-      for (int k = 0; k < 32 / DOWN; ++k) {
-        const int down = k * DOWN + lane / ACROSS, across = lane % ACROSS * PER, t = tb + down, n = nb + across;
-        if (t < p.tokens && n < p.N)
-          *reinterpret_cast<w4*>(y + t * y_row + n) = *reinterpret_cast<const w4*>(mine + down * PITCH + across * sizeof(raw));
+    for (int k = 0; k < 32 / DOWN; ++k) {
+      const int down = k * DOWN + lane / ACROSS, across = lane % ACROSS * PER, t = tb + down, n = nb + across;
+      if (t >= p.tokens || n >= p.N) continue;
+      raw v[PER];
+      *reinterpret_cast<w4*>(v) = *reinterpret_cast<const w4*>(mine + down * PITCH + across * sizeof(raw));
+      if (OUT == kSums || n + PER <= p.N) {
+        __builtin_memcpy(y + t * y_row + n, v, sizeof v);  // at any multiple of an element
+      } else {
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+          if (n + e < p.N) y[t * y_row + n + e] = v[e];
       }
-    } else {  // an element to a lane, so that a wavefront still writes one run
-      for (int down = 0; down < min(32, p.tokens - tb); ++down)
-        for (int n = lane; n < min(FW * 32, p.N - nb); n += 64)
-          y[(tb + down) * y_row + nb + n] = *reinterpret_cast<const raw*>(mine + down * PITCH + n * sizeof(raw));
     }
     wait_lds();
     __builtin_amdgcn_sched_barrier(0);
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(64 * GW * GT, 2) int8_tile_kernel(Product p, T
 }
 
 // Sums of parts of K to outputs, four to a thread.
-template <int OUT, bool WHOLE>
+template <int OUT>
 __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, int64_t first) {
   const int64_t at = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int across = p.pitch / 4, n = 4 * (int)(at % across);
@@ -343,18 +348,15 @@ __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, in
   for (int k = 0; k < parts; ++k) sum += *reinterpret_cast<const i4*>(p.sums + (k * (int64_t)p.tokens + t) * p.pitch + n);
   const float s = p.scale[t];
   typename Elem<OUT>::raw* y = static_cast<typename Elem<OUT>::raw*>(p.y) + t * p.y_row + n;
-  float v[4];
+  typename Elem<OUT>::raw v[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = scaled(p, sum[e], s, min(n + e, p.N - 1));
-  if constexpr (WHOLE) {
-    if constexpr (OUT == CL_F32)
-      *reinterpret_cast<v4*>(y) = v4{v[0], v[1], v[2], v[3]};
-    else
-      *reinterpret_cast<w2*>(y) = w2{down2<OUT>(v[0], v[1]), down2<OUT>(v[2], v[3])};
+  for (int e = 0; e < 4; ++e) v[e] = Elem<OUT>::down(scaled(p, sum[e], s, min(n + e, p.N - 1)));
+  if (n + 4 <= p.N) {
+    __builtin_memcpy(y, v, sizeof v);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (n + e < p.N) y[e] = Elem<OUT>::down(v[e]);
+      if (n + e < p.N) y[e] = v[e];
   }
 }
 
@@ -481,9 +483,8 @@ cl_status check_values(const void* x, int dtype, int K, float clamp) {
 
 template <int IN, int THREADS, int HELD>
 void launch_quant(const void* x, int64_t x_row, int rows, int K, float clamp, int8_t* codes, int64_t row, float* scale, hipStream_t s) {
-  const auto kernel = heads_aligned(x, IN, x_row, 0) ? int8_quant_kernel<IN, THREADS, HELD, true> : int8_quant_kernel<IN, THREADS, HELD, false>;
   in_pieces(rows, THREADS, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)count), dim3(THREADS), 0, s, static_cast<const typename Elem<IN>::raw*>(x), x_row, first, K,
+    hipLaunchKernelGGL((int8_quant_kernel<IN, THREADS, HELD>), dim3((unsigned)count), dim3(THREADS), 0, s, static_cast<const typename Elem<IN>::raw*>(x), x_row, first, K,
                        (int)padded(K), clamp, codes, row, scale);
   });
 }
@@ -612,10 +613,8 @@ void launch_piece(const Product& p, int K, hipStream_t s) {
   const Plan plan = plan_product(p.tokens, p.N, K);
   if (plan.parts == 1) return launch_shape<OUT>(p, plan, s);
   launch_shape<kSums>(p, plan, s);
-  const bool whole = p.N % 4 == 0 && p.y_row % 4 == 0 && aligned_to(p.y, 4 * elem_size(OUT));
-  const auto join = whole ? int8_join_kernel<OUT, true> : int8_join_kernel<OUT, false>;
   in_pieces((int64_t)p.tokens * (p.pitch / 4), 1, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL(join, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, plan.parts, first);
+    hipLaunchKernelGGL((int8_join_kernel<OUT>), dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, plan.parts, first);
   });
 }
 
