@@ -45,6 +45,7 @@ __device__ __forceinline__ void pair_of(int layout, int half, int i, int* a, int
 struct AxisMap {
   int64_t stride;
   int axes, used;
+  uint32_t first[4];  // of[0] to of[7]
   uint16_t of[64];
 };
 
@@ -58,6 +59,12 @@ struct RopeArgs {
   AxisMap axes;  // read with several axes only
 };
 
+// The axes of pairs 8u to 8u + 7.  Those of 64 pairs are in four words, which a lane picks from sooner than it reads them.
+__device__ __forceinline__ uint32_t axes_of_8(const AxisMap& m, int u) {
+  if (u >= 8) return m.of[u];
+  const uint32_t a = u & 2 ? m.first[1] : m.first[0], b = u & 2 ? m.first[3] : m.first[2], w = u & 4 ? b : a;
+  return (u & 1 ? w >> 16 : w) & 0xffff;
+}
 __device__ __forceinline__ int axis_of(const AxisMap& m, int pair) { return m.of[pair >> 3] >> (2 * (pair & 7)) & 3; }
 
 // Any alignment: one thread a pair of channels, rotated or copied.
@@ -101,9 +108,9 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   const bool turned = 16 * u < a.rot;
   int c1 = 16 * u, c2 = c1 + 8;
   if (turned && a.layout == CL_ROPE_HALF) c1 = 8 * u, c2 = c1 + half;
-  const uint32_t of = AXES && turned ? a.axes.of[u] : 0;  // the axes of pairs 8u to 8u + 7
+  const uint32_t of = AXES && turned ? axes_of_8(a.axes, u) : 0;
   const bool one = !AXES || of == (of & 3) * 0x5555;
-  const int p = !turned ? 0 : AXES ? a.positions[(of & 3) * a.axes.stride + t] : a.positions[t];
+  const int p = turned ? a.positions[AXES ? (of & 3) * a.axes.stride + t : t] : 0;
   const auto* x = static_cast<const typename Elem<IN>::raw*>(a.x) + t * a.x_token + h * a.x_head;
   auto* y = static_cast<typename Elem<OUT>::raw*>(a.y) + t * a.y_token + h * a.y_head;
   float v1[HEADS][8], v2[HEADS][8];
@@ -116,9 +123,13 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   if (turned) {
     float2 cs[8];
     if (AXES && !one) {
+      int on[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) on[k] = k < a.axes.axes ? a.positions[k * a.axes.stride + t] : 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int q = a.positions[(of >> (2 * i) & 3) * a.axes.stride + t];
+        const uint32_t axis = of >> (2 * i) & 3;
+        const int q = axis & 2 ? (axis & 1 ? on[3] : on[2]) : (axis & 1 ? on[1] : on[0]);
         cs[i] = q >= 0 && q < a.table_rows ? a.table[(int64_t)q * half + 8 * u + i] : make_float2(kNan, kNan);
       }
     } else if (p >= 0 && p < a.table_rows) {
@@ -154,6 +165,47 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   }
 }
 
+// Many tokens whose positions have several axes: a workgroup has a few tokens, gathers their cosines and sines into LDS, and then goes
+// through their heads in the same pieces.
+constexpr int kTurnPairs = 1024;
+template <int IN, int OUT>
+__global__ void __launch_bounds__(256) rope_axes_kernel(RopeArgs a, int each) {
+  __shared__ __attribute__((aligned(16))) float2 turn[kTurnPairs];
+  const int units = a.dim / 16, half = a.rot / 2, first = blockIdx.x * each, tokens = min(each, a.tokens - first), pieces = a.heads * units;
+  for (int i = threadIdx.x; i < tokens * half; i += 256) {
+    const int k = i / half, pair = i % half;
+    const int p = a.positions[axis_of(a.axes, pair) * a.axes.stride + first + k];
+    turn[i] = p >= 0 && p < a.table_rows ? a.table[(int64_t)p * half + pair] : make_float2(kNan, kNan);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < tokens * pieces; i += 256) {
+    const int k = i / pieces, at = i - k * pieces, h = at / units, u = at - h * units;
+    const auto* x = static_cast<const typename Elem<IN>::raw*>(a.x) + (first + k) * a.x_token + h * a.x_head;
+    auto* y = static_cast<typename Elem<OUT>::raw*>(a.y) + (first + k) * a.y_token + h * a.y_head;
+    const bool turned = 16 * u < a.rot;
+    int c1 = 16 * u, c2 = c1 + 8;
+    if (turned && a.layout == CL_ROPE_HALF) c1 = 8 * u, c2 = c1 + half;
+    float v1[8], v2[8];
+    load8<IN>(x + c1, v1);
+    load8<IN>(x + c2, v2);
+    if (turned) {
+      const float2* cs = turn + k * half + 8 * u;
+      if (a.layout == CL_ROPE_HALF) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) rotate_pair(v1[j], v2[j], cs[j].x, cs[j].y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          rotate_pair(v1[2 * j], v1[2 * j + 1], cs[j].x, cs[j].y);
+          rotate_pair(v2[2 * j], v2[2 * j + 1], cs[4 + j].x, cs[4 + j].y);
+        }
+      }
+    }
+    store8<OUT>(y + c1, v1);
+    store8<OUT>(y + c2, v2);
+  }
+}
+
 // ------------------------------------------------------------------ append
 struct AppendArgs {
   cl_kv_cache c;
@@ -165,13 +217,6 @@ struct AppendArgs {
   int tokens, rot, layout, table_rows, page_shift, side;
   AxisMap axes;  // read with several axes only
 };
-
-// The cosine and sine of pair i of a token whose positions lie in the table.
-template <bool AXES>
-__device__ __forceinline__ float2 cos_sin(const AppendArgs& a, const float2* row, int t, int i) {
-  if constexpr (!AXES) return row[i];
-  return a.table[(int64_t)a.positions[axis_of(a.axes, i) * a.axes.stride + t] * (a.rot / 2) + i];
-}
 
 // Eight channels from `at` of a head at x; VEC: as two 16-byte (fp32) or one load, otherwise one by one.
 template <int IN, bool VEC>
@@ -204,8 +249,22 @@ template <int IN, int KIND, int D, bool VEC, bool AXES>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   constexpr int LANES = D / 8;
   const int row_at = threadIdx.x / LANES, h = (blockIdx.y << a.side) + (row_at & ((1 << a.side) - 1)), which = blockIdx.z;
-  const int t = blockIdx.x * (256 / LANES >> a.side) + (row_at >> a.side);
+  const int tokens = 256 / LANES >> a.side, first = blockIdx.x * tokens, t = first + (row_at >> a.side);
   const int ch = 8 * (threadIdx.x % LANES);
+  // With several axes a token's cosines and sines are gathered once for its heads in the workgroup.
+  __shared__ float2 turn[AXES ? 256 / LANES : 1][D / 2];
+  if constexpr (AXES) {
+    if (which == 0) {
+      const int half = a.rot / 2;
+      for (int i = threadIdx.x; i < tokens * half; i += 256) {
+        const int k = i / half, pair = i % half;
+        if (first + k >= a.tokens) break;
+        const int p = a.positions[axis_of(a.axes, pair) * a.axes.stride + first + k];
+        turn[k][pair] = p >= 0 && p < a.table_rows ? a.table[(int64_t)p * half + pair] : make_float2(0.f, 0.f);
+      }
+      __syncthreads();
+    }
+  }
   if (t >= a.tokens) return;
   const int slot = a.slots[t];
   if (slot < 0 || slot >= a.c.pages << a.page_shift) return;
@@ -214,9 +273,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   channels8<IN, VEC>(x, ch, v);
   if (a.table && which == 0) {
     const int half = a.rot / 2;
-    const float2* cs = a.table;  // one axis: the position's row
+    const float2* cs;
     bool in = true;
     if constexpr (AXES) {
+      cs = turn[row_at >> a.side];
       for (int k = 0; k < a.axes.axes; ++k) {
         const int p = a.positions[k * a.axes.stride + t];
         in = in && (!(a.axes.used >> k & 1) || (p >= 0 && p < a.table_rows));
@@ -224,7 +284,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
     } else {
       const int p = a.positions[t];
       in = p >= 0 && p < a.table_rows;
-      cs += (int64_t)(in ? p : 0) * half;
+      cs = a.table + (int64_t)(in ? p : 0) * half;
     }
     if (!in) {
 #pragma unroll
@@ -236,7 +296,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
         channels8<IN, VEC>(x, low ? ch + half : ch - half, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 c = cos_sin<AXES>(a, cs, t, (low ? ch : ch - half) + i);
+          const float2 c = cs[(low ? ch : ch - half) + i];
           float p1 = low ? v[i] : w[i], p2 = low ? w[i] : v[i];
           rotate_pair(p1, p2, c.x, c.y);
           v[i] = low ? p1 : p2;
@@ -246,7 +306,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
       if (ch < a.rot) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 c = cos_sin<AXES>(a, cs, t, ch / 2 + i);
+          const float2 c = cs[ch / 2 + i];
           rotate_pair(v[2 * i], v[2 * i + 1], c.x, c.y);
         }
       }
@@ -258,7 +318,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
         int c1, c2;
         pair_of(a.layout, half, pr, &c1, &c2);
         float p1 = Elem<IN>::up(x[c1]), p2 = Elem<IN>::up(x[c2]);
-        const float2 c = cos_sin<AXES>(a, cs, t, pr);
+        const float2 c = cs[pr];
         rotate_pair(p1, p2, c.x, c.y);
         v[i] = ch + i == c1 ? p1 : p2;
       }
@@ -373,12 +433,20 @@ void launch_rope(const RopeArgs& a, hipStream_t s) {
     });
   };
   if (a.axes.axes > 1) {
-    if (!vec)
+    const bool many = (int64_t)a.tokens * a.heads >= (1 << 14), wide = IN == CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17);
+    if (!vec) {
       go(rope_pair_kernel<IN, OUT, true>, (int64_t)a.heads * ((a.dim + 1) / 2));
-    else if (IN != CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17))
-      go(rope_kernel<IN, OUT, 2, true>, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
-    else
+    } else if (many && !wide) {
+      // 8192 x 72 heads of 128, bf16, axes in turn: 50.4 us, as with one axis (48.9); by the kernel of few tokens 71, with four times the
+      // pieces to a workgroup 53.  Wide fp32 heads cover the gathering: 82.4 us by the kernel of few tokens, 86.6 here.
+      const int each = std::max(1, std::min(kTurnPairs / (a.rot / 2), 512 / (a.heads * (a.dim / 16))));
+      in_pieces(a.tokens, 256, [&](int64_t first, int64_t count) {
+        hipLaunchKernelGGL((rope_axes_kernel<IN, OUT>), dim3((unsigned)((count + each - 1) / each)), dim3(256), 0, s,
+                           piece_of(a, IN, OUT, first, count), each);
+      });
+    } else {
       go(rope_kernel<IN, OUT, 1, true>, (int64_t)a.heads * (a.dim / 16));
+    }
     return;
   }
   if (!vec)
@@ -507,7 +575,7 @@ namespace {
 
 // The axis of every pair of a rotation over `rot` channels; no sections: one axis.
 cl_status axis_map(const int32_t* sections, int axes, int order, int rot, int tokens, AxisMap* m) {
-  *m = AxisMap{tokens, 1, 1, {}};
+  *m = AxisMap{tokens, 1, 1, {}, {}};
   if (!sections) return CL_OK;
   if (axes < 1 || axes > 4) return fail(CL_EINVAL, "rope: %d axes (1 to 4 are wanted)", axes);
   if (order != CL_ROPE_BLOCKS && order != CL_ROPE_TURNS) return fail(CL_EINVAL, "rope: unknown order %d of the axes", order);
@@ -533,6 +601,7 @@ cl_status axis_map(const int32_t* sections, int axes, int order, int rot, int to
     m->of[i / 8] |= (uint16_t)(axis << (2 * (i % 8)));
     m->used |= 1 << axis;
   }
+  for (int u = 0; u < 8; ++u) m->first[u / 2] |= (uint32_t)m->of[u] << (16 * (u % 2));
   return CL_OK;
 }
 
