@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kMostSequences = 4096;
 constexpr int kMostKept = 256;
+constexpr int kScan = 16384;  // pages that a workgroup looks at together, 16 to a thread
 
 struct Pool {
   int32_t *table, *lens, *refs, *left_out;
@@ -96,7 +97,7 @@ __device__ __forceinline__ int sequence_of(const int* base, int n, int t) {
 
 // ------------------------------------------------------------------- extend
 // One workgroup: every page that is given out depends on how many were before.  A thread has four sequences side by
-// side, so that their order is the threads'.  Pages are found 16384 at a time, lowest first, until there are enough; a free
+// side, so that their order is the threads'.  Pages are found kScan at a time, lowest first, until there are enough; a free
 // page's number among the free ones says whose it is, by a search in the sequences' ends.  Bound by the chain of loads: the
 // sequences' tokens, their last pages, those pages' counts, the pages given, the slots.
 __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t* __restrict__ cu, int tokens,
@@ -106,6 +107,7 @@ __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t
   __shared__ int ends[kMostSequences];   // pages given to it and those before
   __shared__ int from[kMostSequences];   // its first place that is given a page
   __shared__ int base[kMostSequences + 1];  // its first new token's number (cu), or the largest of those before
+  __shared__ int list[kScan];            // free pages, a scan's
   __shared__ int waves[16];
   __shared__ int left;
   const int B = p.sequences, tid = threadIdx.x, page = 1 << p.page_shift;
@@ -174,15 +176,16 @@ __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t
     }
   }
   __syncthreads();
-  // Pages given to places, lowest page first.
+  // Free pages, lowest first, into a list, and from there to places: each thread takes one at a time, whoever found it.
   int found = 0;
-  for (int64_t first = 0; first < p.pages && found < all.all; first += 16384) {
+  for (int64_t first = 0; first < p.pages && found < all.all; first += kScan) {
     const int at = (int)min(first + 16 * tid, (int64_t)p.pages);
     uint32_t bits = first ? sixteen<true>(p.refs, at, p.pages) : free0;
     const Before rank = sum_before(__popc(bits), waves);
-    int k = found + rank.before;
-    for (; bits && k < all.all; bits &= bits - 1, ++k) {
-      const int given = at + __builtin_ctz(bits);
+    for (int k = rank.before; bits && found + k < all.all; bits &= bits - 1, ++k) list[k] = at + __builtin_ctz(bits);
+    __syncthreads();
+    for (int k = found + tid; k < min(found + rank.all, all.all); k += 1024) {
+      const int given = list[k - found];
       int lo = 0, hi = B - 1;  // the first sequence that ends past k
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
@@ -196,9 +199,9 @@ __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t
       p.refs[given] = 1;
     }
     found += rank.all;
+    __syncthreads();
   }
   found = min(found, all.all);
-  __syncthreads();
   // Whoever ends past the pages found is left out, and with it everyone after: what it was given goes back.
   int out = 0;
   end = all.before;
@@ -317,43 +320,49 @@ __global__ void __launch_bounds__(64) pool_truncate_kernel(Pool p, const int32_t
 
 // ------------------------------------------------------------------ compact
 // One workgroup.  With n pages held, those from n on move to the free ones below n: the highest to the lowest, up to
-// `most` of them.  work[page] is where a moved page went, work[pages] the lowest page that moved.
+// `most` of them.  Both lists are found by scans, then a thread takes a move at a time.  work[page] is where a moved page went,
+// work[pages] the lowest page that moved.
 __global__ void __launch_bounds__(1024) pool_compact_kernel(Pool p, int most, int32_t* __restrict__ src,
                                                             int32_t* __restrict__ dst, int32_t* __restrict__ work) {
   __shared__ int waves[16];
   const int tid = threadIdx.x;
+  const uint32_t held0 = sixteen<false>(p.refs, 16 * tid, p.pages);
+  const auto held_at = [&](int64_t first) { return first ? sixteen<false>(p.refs, (int)min(first + 16 * tid, (int64_t)p.pages), p.pages) : held0; };
   int held = 0;
-  for (int64_t first = 16 * tid; first < p.pages; first += 16384) held += __popc(sixteen<false>(p.refs, (int)first, p.pages));
+  for (int64_t first = 0; first < p.pages; first += kScan) held += __popc(held_at(first));
   held = sum_before(held, waves).all;
   int holes = 0;
-  for (int64_t first = 0; first < held; first += 16384) {
-    const int at = (int)min(first + 16 * tid, (int64_t)held);
-    uint32_t bits = sixteen<true>(p.refs, at, held);
+  for (int64_t first = 0; first < held; first += kScan) {
+    const int at = (int)min(first + 16 * tid, (int64_t)held), n = min(16, held - at);
+    uint32_t bits = n > 0 ? ~held_at(first) & (0xffffu >> (16 - n)) : 0;
     const Before rank = sum_before(__popc(bits), waves);
     for (int k = holes + rank.before; bits && k < most; bits &= bits - 1, ++k) dst[k] = at + __builtin_ctz(bits);
     holes += rank.all;
   }
   const int moves = min(holes, most);
-  for (int k = moves + tid; k < most; k += 1024) src[k] = dst[k] = -1;
-  if (tid == 0) work[p.pages] = p.pages;
-  __syncthreads();
   int before = 0;  // held pages from `held` on; there are as many as holes
-  for (int64_t first = held & ~15; first < p.pages; first += 16384) {
-    const int at = (int)min(first + 16 * tid, (int64_t)p.pages);
-    uint32_t bits = sixteen<false>(p.refs, at, p.pages);
+  for (int64_t first = (int64_t)held / kScan * kScan; first < p.pages; first += kScan) {
+    const int64_t at = first + 16 * tid;
+    uint32_t bits = held_at(first);
     if (at < held) bits &= at + 16 <= held ? 0u : ~0u << (held - at);
     const Before rank = sum_before(__popc(bits), waves);
-    for (int k = holes - 1 - before - rank.before; bits; bits &= bits - 1, --k) {
-      if (k >= moves) continue;
-      const int page = at + __builtin_ctz(bits), to = dst[k];
-      src[k] = page;
-      work[page] = to;
-      p.refs[to] = p.refs[page];
-      p.refs[page] = 0;
-      if (k == moves - 1) work[p.pages] = page;
-    }
+    for (int k = holes - 1 - before - rank.before; bits; bits &= bits - 1, --k)
+      if (k < moves) src[k] = (int)at + __builtin_ctz(bits);
     before += rank.all;
   }
+  __syncthreads();
+  for (int k = tid; k < most; k += 1024) {
+    if (k >= moves) {
+      src[k] = dst[k] = -1;
+      continue;
+    }
+    const int from = src[k], to = dst[k];
+    work[from] = to;
+    p.refs[to] = p.refs[from];
+    p.refs[from] = 0;
+    if (k == moves - 1) work[p.pages] = from;
+  }
+  if (tid == 0 && moves == 0) work[p.pages] = p.pages;
 }
 
 __global__ void __launch_bounds__(256) pool_rename_kernel(Pool p, const int32_t* __restrict__ work) {
@@ -397,12 +406,13 @@ __global__ void __launch_bounds__(256) kv_copy_pages_kernel(CopyArgs a) {
 
 // --------------------------------------------------------------------- keep
 // A workgroup has the drafts of a sequence for one head, K or V: all are read before any is written, so a draft may move to
-// another's place.  Rows are 16-byte pieces (int4 heads of 64 have two), up to eight to a thread.
+// another's place.  Rows are 16-byte pieces (int4 heads of 64 have two), HELD of them to a thread.
 struct KeepArgs {
   cl_kv_cache c;
   const int32_t *table, *lens, *kept;
   int width, most, page_shift;
 };
+template <int HELD>
 __global__ void __launch_bounds__(256) kv_keep_kernel(KeepArgs a) {
   const int b = blockIdx.x, h = blockIdx.y, which = blockIdx.z;
   const bool int8 = a.c.kind == CL_KV_INT8;
@@ -425,12 +435,12 @@ __global__ void __launch_bounds__(256) kv_keep_kernel(KeepArgs a) {
   };
   w4* codes = static_cast<w4*>(which ? a.c.v : a.c.k);
   uint16_t* scale = which ? a.c.v_scale : a.c.k_scale;
-  w4 v[8];
-  int64_t to[8];
+  w4 v[HELD];
+  int64_t to[HELD];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < HELD; ++i) {
     to[i] = -1;
-    const int k = i * 256 + threadIdx.x;
+    const int k = i * blockDim.x + threadIdx.x;
     if (k >= a.most * units) continue;
     int64_t from, row;
     move_of(k / units, &from, &row);
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(256) kv_keep_kernel(KeepArgs a) {
   __builtin_amdgcn_s_waitcnt(0);  // every row is in registers before any place is written
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < HELD; ++i)
     if (to[i] >= 0) codes[to[i]] = v[i];
   if (s_to >= 0) {
 #pragma unroll
@@ -589,7 +599,10 @@ extern "C" cl_status cl_kv_keep(const cl_kv_cache* cache, const int32_t* block_t
     return fail(CL_EINVAL, "keep: a pointer is misaligned");
   if (sequences > 65535) return fail(CL_ESIZE, "keep: more than 65535 sequences");
   const KeepArgs a = {*cache, block_table, ctx_lens, kept, table_width, most, __builtin_ctz(cache->page_size)};
-  hipLaunchKernelGGL(kv_keep_kernel, dim3((unsigned)sequences, (unsigned)cache->heads, 2), dim3(256), 0,
+  // as few threads as have a piece: 64 sequences x 8 heads of 8 drafts 3 us with one wavefront to a workgroup, 6 with four
+  const int pieces = most * (cache->kind == CL_KV_INT8 ? cache->dim / 16 : cache->dim / 32), threads = std::min(256, (pieces + 63) / 64 * 64);
+  const auto kernel = pieces <= 256 ? kv_keep_kernel<1> : pieces <= 512 ? kv_keep_kernel<2> : kv_keep_kernel<8>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)sequences, (unsigned)cache->heads, 2), dim3((unsigned)threads), 0,
                      static_cast<hipStream_t>(stream), a);
   return launched("keep");
 }
