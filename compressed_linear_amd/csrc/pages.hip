@@ -96,55 +96,59 @@ __device__ __forceinline__ int sequence_of(const int* base, int n, int t) {
 }
 
 // ------------------------------------------------------------------- extend
-// One workgroup: every page that is given out depends on how many were before.  A thread has four sequences side by
-// side, so that their order is the threads'.  Pages are found kScan at a time, lowest first, until there are enough; a free
+// One workgroup: every page that is given out depends on how many were before.  A thread has up to four sequences
+// side by side, so that their order is the threads'.  Pages are found kScan at a time, lowest first, until there are enough; a free
 // page's number among the free ones says whose it is, by a search in the sequences' ends.  Bound by the chain of loads: the
 // sequences' tokens, their last pages, those pages' counts, the pages given, the slots.
 __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t* __restrict__ cu, int tokens,
                                                            int32_t* __restrict__ slots, int32_t* __restrict__ src,
                                                            int32_t* __restrict__ dst, int inline_slots) {
-  __shared__ int last[kMostSequences];   // a sequence's last page where its tokens join it, -1
+  __shared__ __attribute__((aligned(16))) int last[kMostSequences];   // a sequence's last page where its tokens join it, -1
   __shared__ int ends[kMostSequences];   // pages given to it and those before
   __shared__ int from[kMostSequences];   // its first place that is given a page
   __shared__ int base[kMostSequences + 1];  // its first new token's number (cu), or the largest of those before
   __shared__ int list[kScan];            // free pages, a scan's
   __shared__ int waves[16];
   __shared__ int left;
-  const int B = p.sequences, tid = threadIdx.x, page = 1 << p.page_shift;
-  uint32_t free0 = sixteen<true>(p.refs, 16 * tid, p.pages);  // asked for before anything is known
-  int len[4], more[4], want[4], mine[4];
+  const int B = p.sequences, tid = threadIdx.x, page = 1 << p.page_shift, per = (B + 1023) / 1024;
+  const auto sequence = [&](int i) { return i < per ? per * tid + i : B; };  // a thread's, B where it has none
+  const uint32_t free0 = sixteen<true>(p.refs, 16 * tid, p.pages);  // asked for before anything is known, as are the next three
+  int len[4], more[4], want[4], mine[4], holders[4];
   bool go[4], any[4];
   for (int b = tid; b <= B; b += 1024) base[b] = cu[b];
-  if (tid == 0) left = 0;
-  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int b = 4 * tid + i;
-    more[i] = b < B ? base[b] : 0;
-    want[i] = b < B ? base[b + 1] : 0;
+    const int b = sequence(i);
+    len[i] = b < B ? p.lens[b] : -1;
+    more[i] = b < B ? cu[b] : 0;
+    want[i] = b < B ? cu[b + 1] : 0;
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int place = len[i] >> p.page_shift;
+    const bool part = len[i] > 0 && len[i] & (page - 1) && place < p.width;
+    mine[i] = part ? p.table[(int64_t)sequence(i) * p.width + place] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) holders[i] = p.has(mine[i]) ? p.refs[mine[i]] : 0;
+  if (tid == 0) left = 0;
   __syncthreads();
   running_max<1024>(base, B + 1, waves);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int b = 4 * tid + i;
+    const int b = sequence(i);
     const int a = more[i], z = want[i];
-    go[i] = false;
-    mine[i] = -1;
     any[i] = a != z;
-    len[i] = more[i] = want[i] = 0;
+    more[i] = want[i] = 0;
+    go[i] = false;
     if (b >= B) continue;
     const bool fits = a >= 0 && a == base[b] && z >= a && z <= tokens;
     more[i] = fits ? z - a : 0;
-    len[i] = p.lens[b];
     go[i] = more[i] > 0 && len[i] >= 0 && (int64_t)len[i] + more[i] <= (int64_t)p.width << p.page_shift;
-    if (go[i] && (len[i] & (page - 1))) {
-      mine[i] = p.table[(int64_t)b * p.width + (len[i] >> p.page_shift)];
-      go[i] = p.has(mine[i]);
-    }
+    if (go[i] && (len[i] & (page - 1))) go[i] = p.has(mine[i]);
     if (!go[i]) mine[i] = -1;
     last[b] = mine[i];
-    want[i] = p.held(len[i] + more[i]) - p.held(len[i]);
+    want[i] = go[i] ? p.held(len[i] + more[i]) - p.held(len[i]) : 0;
   }
   __syncthreads();
   // A last page that others hold too is copied, but for the last of its holders if all of them are extended: k extended
@@ -153,22 +157,27 @@ __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t
   int need = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int b = 4 * tid + i;
+    const int b = sequence(i);
     shared[i] = false;
     if (mine[i] >= 0) {
-      int holders = p.refs[mine[i]];
-      if (holders > 1)
-        for (int j = 0; j < b; ++j) holders -= last[j] == mine[i];
-      shared[i] = holders > 1;
+      if (holders[i] > 1) {
+        int j = 0;
+        for (; j + 4 <= b; j += 4) {
+          const int4 v = *reinterpret_cast<const int4*>(last + j);
+          holders[i] -= (v.x == mine[i]) + (v.y == mine[i]) + (v.z == mine[i]) + (v.w == mine[i]);
+        }
+        for (; j < b; ++j) holders[i] -= last[j] == mine[i];
+      }
+      shared[i] = holders[i] > 1;
     }
-    want[i] = go[i] ? want[i] + shared[i] : 0;
+    want[i] += shared[i];
     need += want[i];
   }
   const Before all = sum_before(need, waves);
   int end = all.before;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int b = 4 * tid + i;
+    const int b = sequence(i);
     end += want[i];
     if (b < B) {
       ends[b] = end;
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t
   end = all.before;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int b = 4 * tid + i;
+    const int b = sequence(i);
     if (b >= B) continue;
     const int start = end;
     end += want[i];
