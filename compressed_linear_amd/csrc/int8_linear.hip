@@ -542,7 +542,7 @@ constexpr Shape kShapes[] = {{256, 256, 1, 1.72f}, {256, 192, 1, 1.45f}, {256, 1
                              {128, 64, 2, 0.46f},  {64, 64, 2, 0.265f},  {64, 32, 3, 0.235f}};
 constexpr int kShapeCount = sizeof kShapes / sizeof kShapes[0], kHalf = 2;
 
-int64_t tiles_of(const Shape& s, int tokens, int N) { return (int64_t)((tokens + s.tt - 1) / s.tt) * ((N + s.tw - 1) / s.tw); }
+int64_t tiles_of(const Shape& s, int tokens, int N) { return (((int64_t)tokens + s.tt - 1) / s.tt) * ((N + s.tw - 1) / s.tw); }
 
 // Half of the last round's tiles or fewer: each is cut in two, so that the round takes half the time.
 bool halved(int64_t tiles) { return tiles % kCus && tiles % kCus <= kCus / 2; }
@@ -609,24 +609,22 @@ void launch_stream(const Product& p, hipStream_t s) {
   hipLaunchKernelGGL((int8_stream_kernel<OUT, WAVES, DEPTH, TR>), dim3((unsigned)((p.N + 15) / 16)), dim3(64 * WAVES), 0, s, p);
 }
 
+// Tokens past what a launch holds (2^22 tiles of 512 threads) go in pieces, which have tiles enough without parts of K.
 template <int OUT>
-void launch_piece(const Product& p, int K, hipStream_t s) {
+void launch_linear(const Product& p, int K, hipStream_t s) {
   // eight wavefronts with three buffers: one token of 8192 x 10240 15.4 us, four with three or four 16.5, sixteen 18; with more token rows
   // two buffers (16 tokens of 8192 x 28672 40.9 us, three 48) and four wavefronts (32 tokens of 4096 x 11008 14.9, eight 17.4)
   if (p.tokens <= 8) return launch_stream<OUT, 8, 3, 8>(p, s);
   if (p.tokens <= 16) return launch_stream<OUT, 8, 2, 16>(p, s);
   if (streamed(p.tokens, p.N, K)) return p.tokens <= 32 ? launch_stream<OUT, 4, 2, 32>(p, s) : launch_stream<OUT, 4, 2, 64>(p, s);
   const Plan plan = plan_product(p.tokens, p.N, K);
-  if (plan.parts == 1) return launch_shape<OUT>(p, plan, s);
-  launch_shape<kSums>(p, plan, s);
-  in_pieces((int64_t)p.tokens * (p.pitch / 4), 1, [&](int64_t first, int64_t count) {
-    hipLaunchKernelGGL((int8_join_kernel<OUT>), dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, plan.parts, first);
-  });
-}
-
-// Tokens past what a launch holds (2^22 tiles of 512 threads) go in pieces.
-template <int OUT>
-void launch_linear(const Product& p, int K, hipStream_t s) {
+  if (plan.parts > 1) {
+    launch_shape<kSums>(p, plan, s);
+    in_pieces((int64_t)p.tokens * (p.pitch / 4), 1, [&](int64_t first, int64_t count) {
+      hipLaunchKernelGGL((int8_join_kernel<OUT>), dim3((unsigned)((count + 255) / 256)), dim3(256), 0, s, p, plan.parts, first);
+    });
+    return;
+  }
   const int64_t most = std::max<int64_t>(1, (1 << 22) / ((p.N + 127) / 128) / 16) * 2048;
   for (int64_t first = 0; first < p.tokens; first += most) {
     Product q = p;
@@ -634,7 +632,7 @@ void launch_linear(const Product& p, int K, hipStream_t s) {
     q.scale += first;
     q.y = beyond(p.y, OUT, first * p.y_row);
     q.tokens = (int)std::min(most, p.tokens - first);
-    launch_piece<OUT>(q, K, s);
+    launch_shape<OUT>(q, plan, s);
   }
 }
 

@@ -88,18 +88,18 @@ _pack_rope_axes, _pack_append_axes, _pack_copy_pages, _pack_keep, _pack_extend, 
 
 _torch = None
 _lib = None
-_empty = _current_device = _raw_stream = _capturing = _i32 = None
+_empty = _split = _current_device = _raw_stream = _capturing = _i32 = None
 _DT: dict = {}
 
 
 def _setup():
     """torch and the library, loaded at the first call (importing the package needs neither)."""
-    global _torch, _lib, _empty, _current_device, _raw_stream, _capturing, _i32
+    global _torch, _lib, _empty, _split, _current_device, _raw_stream, _capturing, _i32
     if _lib is None:
         import torch
 
         from . import lib
-        _torch, _empty, _i32 = torch, torch.empty, torch.int32
+        _torch, _empty, _split, _i32 = torch, torch.empty, torch.split_with_sizes, torch.int32
         # the device's number without a check that torch is set up (0.2 us of a call: the tensors are there), the stream's
         # address without a Stream object around it (1.8 us), where torch has those
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -430,7 +430,7 @@ class PagePool:
                                                 at + 4 * (tokens + B), _stream(dev)))
         if st:
             _check(st, "cl_pool_extend")
-        return buf[:tokens], buf[tokens:tokens + B], buf[tokens + B:]
+        return _split(buf, (tokens, B, B))  # half the time of three slices
 
     def fork(self, parents):
         """Every sequence b at once becomes what sequence parents[b] (int32 [sequences]) was, sharing its pages
@@ -462,7 +462,7 @@ class PagePool:
         st = _lib.cl_call(_COMPACT, _pack_compact(self._ref, n, at, at + 4 * n, at + 8 * n, size, _stream(dev)))
         if st:
             _check(st, "cl_pool_compact")
-        return buf[:n], buf[n:2 * n]
+        return _split(buf, (n, n, self.pages + 1))[:2]
 
 
 def tree_attention(q, cache: KVCache, block_table, ctx_lens, cu_q, max_q: int, max_ctx: Optional[int] = None,

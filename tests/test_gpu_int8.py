@@ -202,6 +202,27 @@ def test_stream_and_graph():
             assert torch.equal(y, eager), k
 
 
+def test_more_tiles_than_a_launch_holds():
+    # 137 GB of outputs: two pieces of tokens, the second of 20
+    torch = torch_cuda()
+    N, K, T = 1 << 23, 128, 8192 + 20
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("not enough memory")
+    r = np.random.default_rng(1)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda")
+    ws = torch.rand(N, device="cuda")
+    layer = cla.Int8Linear(w, ws)
+    x = values(r, (T, K), "f16")
+    say("pieces", T, K, N)
+    y = layer(x, out_dtype=torch.float16)
+    q, s = ref.quantise(x.float().cpu().numpy())
+    for t in (slice(0, 3), slice(8190, 8195), slice(T - 3, T)):
+        for n in (slice(0, 300), slice(N // 2, N // 2 + 300), slice(N - 300, N)):
+            check(y[t, n], q[t], s[t], w[n].cpu().numpy(), ws[n].cpu().numpy(), None, "f16")
+    del y
+    torch.cuda.empty_cache()
+
+
 def test_refusals():
     torch = torch_cuda()
     dev = "cuda"
