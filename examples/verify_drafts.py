@@ -100,11 +100,8 @@ class Block:
     def keep(self, path):
         """Moves the accepted drafts' entries together: they are quantised as they are, so codes and scales are copied."""
         if path:
-            dev = self.embed.device
-            src = self.slots(self.n + torch.tensor(path, device=dev)).long()
-            dst = self.slots(self.n + torch.arange(len(path), device=dev)).long()
-            for t in (self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale):
-                t[dst // PAGE, :, dst % PAGE] = t[src // PAGE, :, src % PAGE]
+            at = torch.tensor([self.n], dtype=torch.int32, device=self.embed.device)
+            self.cache.keep(self.pages, at, torch.tensor([path], dtype=torch.int32, device=self.embed.device))
         self.n += len(path)
 
 
