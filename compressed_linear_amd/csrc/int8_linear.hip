@@ -319,13 +319,14 @@ __device__ __forceinline__ int of_xcd(int id, int n) {
   const int xcd = id & 7, each = n >> 3, extra = n & 7;
   return xcd * each + min(xcd, extra) + (id >> 3);
 }
-// The ring of a step's rows, or 32 rows of each wavefront's outputs.
-constexpr int lds_bytes(int rows, int depth, int waves, int out) {
-  return depth * rows * 128 > waves * 32 * (out + 16) ? depth * rows * 128 : waves * 32 * (out + 16);
+// The rings' rows of 128 bytes, or 32 rows of each wavefront's outputs.
+constexpr int lds_bytes(int rows, int half_rows, int waves, int out) {
+  const int ring = 128 * (rows > half_rows ? rows : half_rows), outputs = waves * 32 * (out + 16);
+  return ring > outputs ? ring : outputs;
 }
 template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool HALVES, bool ONCE>
 __global__ void __launch_bounds__(64 * GW * GT, 2) int8_tile_kernel(Product p, Tiles g) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[lds_bytes(TW + TT, DEPTH, GW * GT, TW / GW * (int)sizeof(typename Result<OUT>::raw))];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[lds_bytes((TW + TT) * DEPTH, (TW + TT / 2) * (HALVES ? DEPTH + 1 : 0), GW * GT, TW / GW * (int)sizeof(typename Result<OUT>::raw))];
   const bool half = HALVES && (int)blockIdx.x >= g.full;
   const int unit = half ? of_xcd(blockIdx.x - g.full, gridDim.x - g.full) : of_xcd(blockIdx.x, HALVES ? g.full : gridDim.x);
   const int tiles = g.t * g.w, at = half ? g.full + (unit >> 1) : unit, part = at / tiles, number = at % tiles;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(64 * GW * GT, 2) int8_tile_kernel(Product p, T
   if constexpr (HALVES) {
     if (half) {
       const int t = t0 + (unit & 1) * (TT / 2);
-      if (t < p.tokens) tile<OUT, TW, TT / 2, GW, GT, DEPTH, ONCE>(p, lds, t, n0, first, end, part);
+      if (t < p.tokens) tile<OUT, TW, TT / 2, GW, GT, DEPTH + 1, ONCE>(p, lds, t, n0, first, end, part);
       return;
     }
   }
