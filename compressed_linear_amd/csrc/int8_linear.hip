@@ -169,7 +169,10 @@ __device__ __forceinline__ void meet() {
 // directly, DEPTH - 1 steps ahead, into a ring of DEPTH buffers; a row's eight pieces of 16 bytes lie permuted by (row / 2) % 8, so that the 16
 // lanes which LDS serves at once read all its banks.  A quarter step's operands are read between the products of the one before.  The
 // one barrier of a step stands before its last quarter, whose operands are in registers: behind it the next buffer has arrived
-// everywhere and this one is read by nobody.  Rows past the last give zeros (buffer loads with their bounds), and so do steps.
+// everywhere and this one is read by nobody.  Rows past the last and steps past the end are not read (the loads know their buffer's size), and
+// what LDS holds in their place reaches no output.  ONCE: the weights are not kept in the caches, since no other tile reads them.
+// Bound by power and by waiting for memory about equally where there are many tiles (2048 x 8192 x 28672, 411 us, 2.34 POPS: the matrix
+// cores busy 55 % of the time, the clock at 1.9 of 2.4 GHz; with codes of zeros 2.4 GHz), by waiting where there are few.
 template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool ONCE>
 __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int n0, int first, int end, int part) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -326,7 +329,8 @@ constexpr int lds_bytes(int rows, int half_rows, int waves, int out) {
 }
 template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool HALVES, bool ONCE>
 __global__ void __launch_bounds__(64 * GW * GT, 2) int8_tile_kernel(Product p, Tiles g) {
-  __shared__ __attribute__((aligned(128))) uint8_t lds[lds_bytes((TW + TT) * DEPTH, (TW + TT / 2) * (HALVES ? DEPTH + 1 : 0), GW * GT, TW / GW * (int)sizeof(typename Result<OUT>::raw))];
+  __shared__ __attribute__((aligned(128))) uint8_t lds[lds_bytes((TW + TT) * DEPTH, (TW + TT / 2) * (HALVES ? DEPTH + 1 : 0), GW * GT,
+                                                                 TW / GW * (int)sizeof(typename Result<OUT>::raw))];
   const bool half = HALVES && (int)blockIdx.x >= g.full;
   const int unit = half ? of_xcd(blockIdx.x - g.full, gridDim.x - g.full) : of_xcd(blockIdx.x, HALVES ? g.full : gridDim.x);
   const int tiles = g.t * g.w, at = half ? g.full + (unit >> 1) : unit, part = at / tiles, number = at % tiles;
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, in
 }
 
 // ------------------------------------------------------------- few tokens
-// Few tokens: the weights are read once.  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
+// Few tokens: the weights are read once, which bounds it (one token of 8192 x 28672 37 us, 6.3 TB/s).  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
 // ring of DEPTH buffers in LDS to itself, so that they wait for their own loads only, and their sums meet in LDS at the end
 // (v_mfma_i32_16x16x64_i8, weights as the first operand).  Rows lie as in a tile; TR (8, or a multiple of 16) token rows come with the weights.
 template <int OUT, int WAVES, int DEPTH, int TR>
@@ -521,11 +525,12 @@ void launch_quant(const void* x, int dtype, int64_t x_row, int rows, int K, floa
 
 // ------------------------------------------------------------------- plan
 constexpr int kCus = 256;
+constexpr int kMostParts = 16;
+
 // What int8_stream_kernel takes: up to 16 tokens, and up to 64 with few weights, where reading the tokens once for every 16 outputs costs
 // less than the start of tiles (32 tokens of 4096 x 4096 6.7 us, as tiles 10; 64 8.8 and 10.7; of 4096 x 11008 14.9 and 12.7, of
 // 11008 x 4096 64 18.4 and 16.3).
 bool streamed(int tokens, int N, int K) { return tokens <= 16 || (tokens <= 64 && (int64_t)N * K <= 1 << 25); }
-constexpr int kMostParts = 16;
 
 // How a product is cut: the tile, parts of K.
 struct Plan {
@@ -545,12 +550,13 @@ constexpr int kShapeCount = sizeof kShapes / sizeof kShapes[0], kHalf = 2;
 
 int64_t tiles_of(const Shape& s, int tokens, int N) { return (((int64_t)tokens + s.tt - 1) / s.tt) * ((N + s.tw - 1) / s.tw); }
 
-// Half of the last round's tiles or fewer: each is cut in two, so that the round takes half the time.
+// Half of the last round's tiles or fewer: each is cut in two, with a buffer more, so that the round is shorter (2048 x 8192 x 28672 has 3.5
+// rounds: 423 us; with two buffers 452, with whole tiles 459).
 bool halved(int64_t tiles) { return tiles % kCus && tiles % kCus <= kCus / 2; }
 
 // The cheapest of the tiles and parts of K by those costs: steps x tiles of the busiest CU, 3.5 us to fill and to empty each, at least the
-// time to read the weights (8 bytes a picosecond is more than memory gives: it ranks the small products), and for parts 4 us and the sums
-// written and read at 4.2 bytes a picosecond.  Over 100 products of 24 to 4096 tokens and 1000 x 1000 to 8192 x 28672 weights the choice
+// time to read the weights (8 TB/s is more than memory gives: it ranks the small products), and for parts 4 us and the sums
+// written and read at 4.2 TB/s.  Over 100 products of 24 to 4096 tokens and 1000 x 1000 to 8192 x 28672 weights the choice
 // is 2 % slower than the best of all in the mean, 25 % at worst; 256 x 256 tiles alone would be up to eight times slower.
 Plan plan_product(int tokens, int N, int K) {
   Plan best;

@@ -34,7 +34,7 @@ def check(y, q, s, w, ws, bias, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("T,K", [(1, 1), (1, 4096), (3, 5), (2, 127), (5, 129), (37, 1000), (300, 384), (2, 28672), (9, 10241)])
+@pytest.mark.parametrize("T,K", [(1, 1), (1, 4096), (3, 5), (2, 127), (5, 129), (37, 1000), (300, 384), (2, 28672), (9, 10241), (3, 40001), (1, 131071)])
 def test_codes(T, K, dtype):
     torch = torch_cuda()
     r = np.random.default_rng(K * 10 + T)
