@@ -53,7 +53,8 @@ def _clamp(clamp):
     c = 0.0 if clamp is None else float(clamp)
     if clamp is not None and not 0.0 < c < 3.4e38:
         raise ValueError("clamp must be positive and finite (None: no clamp)")
-    return c
+    # The entries take 0 as no clamp, which a clamp below the least float would become; all clamps below 2^-100 give zeros.
+    return max(c, 2.0 ** -126) if clamp is not None else 0.0
 
 
 def quantize_rows(x, clamp: Optional[float] = None):

@@ -54,7 +54,7 @@ cl_status cl_int8_linear(const int8_t* codes, int64_t row, const float* scale, i
                          int32_t y_dtype, int64_t y_row, void* work, size_t work_bytes, void* stream);
 
 /*
- * cl_int8_forward -- cl_int8_quant and cl_int8_linear in one call, and in one launch for a few tokens.
+ * cl_int8_forward -- cl_int8_quant and cl_int8_linear in one call.
  *   work             device, cl_int8_work_bytes(tokens, N, K, 0) bytes, as for cl_int8_linear
  * Errors: as both.
  */

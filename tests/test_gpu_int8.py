@@ -246,3 +246,15 @@ def test_refusals():
             call()
     assert cla.quantize_rows(x[:0])[0].shape == (0, 64)
     assert layer.forward_codes(codes[:0], scale[:0]).shape == (0, 8)
+
+
+@pytest.mark.parametrize("clamp", [2.0 ** -101, 1e-45, 1e-50])
+def test_clamps_below_the_least_scale_leave_zeros(clamp):
+    """Every value is clamped below 2^-100, so codes and scales are zeros and a layer's outputs are its bias."""
+    torch = torch_cuda()
+    x = torch.linspace(-3, 3, 5 * 130, device="cuda").reshape(5, 130)
+    codes, scale = cla.quantize_rows(x, clamp=clamp)
+    assert not codes.any() and not scale.any()
+    bias = torch.arange(7, dtype=torch.float32, device="cuda")
+    layer = cla.Int8Linear.from_weight(torch.ones(7, 130, device="cuda"), bias=bias, clamp=clamp)
+    assert torch.equal(layer(x), bias.expand(5, 7))

@@ -2,6 +2,8 @@
 import ctypes
 import os
 
+import pytest
+
 import compressed_linear_amd as cla
 from test_abi import ROOT, header_functions
 
@@ -60,3 +62,10 @@ def test_linear_refuses():
     need = L.cl_int8_work_bytes(200, 1000, 100000, 1)
     assert need >= 2 * 4 * 200 * 1000 and need < L.cl_int8_work_bytes(200, 1000, 100000, 0)
     assert linear(tokens=200, N=1000, K=100000, row=100096, w_row=100096, size=need - 1) == -3
+
+
+@pytest.mark.parametrize("clamp", [1e-30, 1e-45, 1e-50, 5e-324])
+def test_a_small_clamp_stays_one(clamp):
+    """The entries take a clamp of 0 as none, so one that a float cannot hold must not become 0."""
+    from compressed_linear_amd.int8 import _clamp
+    assert ctypes.c_float(_clamp(clamp)).value > 0.0
