@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(256) int8_join_kernel(Product p, int parts, in
 }
 
 // ------------------------------------------------------------- few tokens
-// Few tokens: the weights are read once, which bounds it (one token of 8192 x 28672 37 us, 6.3 TB/s).  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
+// Few tokens: the weights are read once, which bounds it (one token of 8192 x 28672 37.5 us, 6.3 TB/s).  A workgroup has 16 outputs; its wavefronts take the steps of 128 k in turn, each with a
 // ring of DEPTH buffers in LDS to itself, so that they wait for their own loads only, and their sums meet in LDS at the end
 // (v_mfma_i32_16x16x64_i8, weights as the first operand).  Rows lie as in a tile; TR (8, or a multiple of 16) token rows come with the weights.
 template <int OUT, int WAVES, int DEPTH, int TR>

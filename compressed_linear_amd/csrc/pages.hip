@@ -99,7 +99,8 @@ __device__ __forceinline__ int sequence_of(const int* base, int n, int t) {
 // One workgroup: every page that is given out depends on how many were before.  A thread has up to four sequences
 // side by side, so that their order is the threads'.  Pages are found kScan at a time, lowest first, until there are enough; a free
 // page's number among the free ones says whose it is, by a search in the sequences' ends.  Bound by the chain of loads: the
-// sequences' tokens, their last pages, those pages' counts, the pages given, the slots.
+// sequences' tokens, their last pages, those pages' counts, the pages given, the slots (8.5 us for 64 sequences of 16 drafts; a scan past
+// held pages is 1.8 us for each kScan of them).
 __global__ void __launch_bounds__(1024) pool_extend_kernel(Pool p, const int32_t* __restrict__ cu, int tokens,
                                                            int32_t* __restrict__ slots, int32_t* __restrict__ src,
                                                            int32_t* __restrict__ dst, int inline_slots) {
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(256) pool_slots_kernel(Pool p, const int32_t* 
 
 // --------------------------------------------------------------------- fork
 // A workgroup has some places of all sequences: it reads them all before it writes any, so that sequences can take each
-// other's rows.  The first one has the lengths too.
+// other's rows.  The first one has the lengths too.  Bound by the chain of loads and the holders' counts (4.3 us for 64 sequences).
 constexpr int kForkWords = 16384;
 __global__ void __launch_bounds__(1024) pool_fork_kernel(Pool p, const int32_t* __restrict__ parents, int columns) {
   __shared__ int old[kForkWords];
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(1024) pool_fork_kernel(Pool p, const int32_t* 
 }
 
 // ----------------------------------------------------------------- truncate
+// A wavefront a sequence, since a sequence gives back few pages at a time.  Bound by the launch (1.4 to 3.3 us).
 __global__ void __launch_bounds__(64) pool_truncate_kernel(Pool p, const int32_t* __restrict__ to) {
   const int b = blockIdx.x, len = p.lens[b], n = to[b];
   if (n < 0 || n >= len) return;
@@ -330,7 +332,8 @@ __global__ void __launch_bounds__(64) pool_truncate_kernel(Pool p, const int32_t
 // ------------------------------------------------------------------ compact
 // One workgroup.  With n pages held, those from n on move to the free ones below n: the highest to the lowest, up to
 // `most` of them.  Both lists are found by scans, then a thread takes a move at a time.  work[page] is where a moved page went,
-// work[pages] the lowest page that moved.
+// work[pages] the lowest page that moved.  Bound by the scans and the moves' loads (8.9 us for 2948 moves); the table's new names
+// are a launch of their own, all of its entries side by side (4.8 us).
 __global__ void __launch_bounds__(1024) pool_compact_kernel(Pool p, int most, int32_t* __restrict__ src,
                                                             int32_t* __restrict__ dst, int32_t* __restrict__ work) {
   __shared__ int waves[16];
@@ -382,7 +385,8 @@ __global__ void __launch_bounds__(256) pool_rename_kernel(Pool p, const int32_t*
 }
 
 // --------------------------------------------------------------- copy pages
-// A page of a cache is four runs of bytes (codes and scales of K and V); a workgroup copies one piece of one of them.
+// A page of a cache is four runs of bytes (codes and scales of K and V); a workgroup copies one piece of one of them, four loads of 16 bytes
+// under way in a thread.  Bound by memory (2948 pages of 133 KB 152 to 155 us, 5.2 TB/s read and written).
 struct CopyArgs {
   const int32_t *src, *dst;
   uint8_t* run[4];
