@@ -283,17 +283,19 @@ __global__ void __launch_bounds__(256) pool_slots_kernel(Pool p, const int32_t* 
 
 // --------------------------------------------------------------------- fork
 // A workgroup has some places of all sequences: it reads them all before it writes any, so that sequences can take each
-// other's rows.  The first one has the lengths too.  Bound by the chain of loads and the holders' counts (4.3 us for 64 sequences).
+// other's rows.  Of all workgroups the first one has the lengths too; `block` are in launches before this one.  Bound by the chain of
+// loads and the holders' counts (4.3 us for 64 sequences).
 constexpr int kForkWords = 16384;
-__global__ void __launch_bounds__(1024) pool_fork_kernel(Pool p, const int32_t* __restrict__ parents, int columns) {
+__global__ void __launch_bounds__(1024) pool_fork_kernel(Pool p, const int32_t* __restrict__ parents, int columns, int block) {
   __shared__ int old[kForkWords];
-  const int B = p.sequences, first = blockIdx.x * columns, n = min(columns, p.width - first);
+  block += blockIdx.x;
+  const int B = p.sequences, first = block * columns, n = min(columns, p.width - first);
   for (int i = threadIdx.x; i < B * n; i += 1024) old[i] = p.table[(int64_t)(i / n) * p.width + first + i % n];
   int lens[kMostSequences / 1024];
 #pragma unroll
   for (int i = 0; i < kMostSequences / 1024; ++i) {
     const int b = i * 1024 + threadIdx.x;
-    if (blockIdx.x || b >= B) continue;
+    if (block || b >= B) continue;
     const int from = parents[b];
     lens[i] = from >= 0 && from < B ? p.lens[from] : 0;
   }
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(1024) pool_fork_kernel(Pool p, const int32_t* 
 #pragma unroll
   for (int i = 0; i < kMostSequences / 1024; ++i) {
     const int b = i * 1024 + threadIdx.x;
-    if (blockIdx.x == 0 && b < B) p.lens[b] = lens[i];
+    if (block == 0 && b < B) p.lens[b] = lens[i];
   }
 }
 
@@ -529,8 +531,11 @@ extern "C" cl_status cl_pool_fork(const cl_page_pool* pool, const int32_t* paren
   if (st != CL_OK) return st;
   if (!parents || !aligned_to(parents, 4)) return fail(CL_EINVAL, "fork: parents is NULL or misaligned");
   const int columns = std::min(16, kForkWords / p.sequences);
-  hipLaunchKernelGGL(pool_fork_kernel, dim3((unsigned)((p.width + columns - 1) / columns)), dim3(1024), 0,
-                     static_cast<hipStream_t>(stream), p, parents, columns);
+  // tables of 2^26 places and more have more threads than a launch
+  in_pieces(((int64_t)p.width + columns - 1) / columns, 1024, [&](int64_t first, int64_t count) {
+    hipLaunchKernelGGL(pool_fork_kernel, dim3((unsigned)count), dim3(1024), 0, static_cast<hipStream_t>(stream), p, parents, columns,
+                       (int)first);
+  });
   return launched("fork");
 }
 
