@@ -164,7 +164,8 @@ def _axes(positions, T, sections, dev):
     if host is None:
         if min(pairs) < 0 or sum(pairs) > 512:
             raise ValueError("sections are pairs of up to 1024 channels")
-        host = _sections[key] = pairs, pairs.buffer_info()[0]
+        # another thread may have kept its own by now, and this one would not outlive the call
+        host = _sections.setdefault(key, (pairs, pairs.buffer_info()[0]))
     return _index(positions, axes * T, dev, "positions"), axes, host[1]
 
 
