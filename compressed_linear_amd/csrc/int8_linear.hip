@@ -140,8 +140,10 @@ struct Result<kSums> {
   typedef int32_t raw;
 };
 
+// Each product and the sum rounded to fp32 (no fused multiply-add), so that every kernel gives a row the same bits.
 __device__ __forceinline__ float scaled(const Product& p, int sum, float s, int n) {
-  float v = (float)sum * s * p.w_scale[n];
+#pragma clang fp contract(off)
+  const float v = (float)sum * s * p.w_scale[n];
   return p.bias ? v + p.bias[n] : v;
 }
 
