@@ -420,7 +420,8 @@ class PagePool:
         `tree_attention`), `tokens` in all.  Returns (slots int32 [tokens], src, dst int32 [sequences]): the tokens'
         places, for KVCache.append, and the pages that KVCache.copy_pages has to copy before, in every cache, since
         other sequences hold them too.  A sequence that there is no room for stays as it was, its slots are -1, and
-        left_out counts it."""
+        left_out counts it; the others have room and copies all the same, so a pass that is given up then copies their pages
+        and gives the room back by `truncate`."""
         dev = self.device
         if tokens < 0:
             raise ValueError("tokens must be >= 0")

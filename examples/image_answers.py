@@ -45,7 +45,7 @@ class Answers:
 
     def forward(self, hidden, counts, positions, tree_mask=None):
         """Logits of the sequences' new tokens (hidden [tokens, HIDDEN], counts of each sequence, positions [3, tokens]); they join
-        the cache."""
+        the cache.  Where one of them has no room none does, and the sequences stay as they were."""
         T, dev = len(hidden), self.device
         if sum(counts) != T:
             raise ValueError("%d tokens, but %d are counted" % (T, sum(counts)))
@@ -53,9 +53,10 @@ class Answers:
         cu = torch.tensor([0] + counts, dtype=torch.int32, device=dev).cumsum(0).to(torch.int32)
         before = self.pool.lens.clone()
         slots, src, dst = self.pool.extend(cu, T)
-        if int(self.pool.left_out):
-            raise RuntimeError("no pages are left")
         self.cache.copy_pages(src, dst)
+        if int(self.pool.left_out):  # the others have their room and their copies already: what they got is given back
+            self.pool.truncate(before)
+            raise RuntimeError("no pages are left")
         position = positions.to(torch.int32).contiguous()
         qkv = self.qkv(norm(hidden)).view(T, Q_HEADS + 2 * KV_HEADS, DIM)  # fp32
         q = cla.rope(qkv[:, :Q_HEADS], position, self.rope, out_dtype=torch.float16, sections=SECTIONS, order=ORDER)
