@@ -88,7 +88,7 @@ def _whole_rows(codes):
         and end <= codes.untyped_storage().nbytes(), row
 
 
-class Int8Linear:
+class Int8Linear(_s._Fixed):
     """A linear layer in 8-bit integers on one GPU: y[t, n] = (sum_k a[t, k] w[n, k]) s[t] scale[n] + bias[n], the
     sum exact in 32-bit integers, a and s the token's codes and scale (quantize_rows).
 
@@ -96,6 +96,8 @@ class Int8Linear:
     activations are clipped to [-clamp, clamp] before they are quantised.  Codes whose K is a multiple of 128 are used as they
     are; others are copied into rows padded with zeros.
     """
+
+    _fixed = frozenset(("codes", "scale", "bias", "clamp", "N", "K", "device"))
 
     def __init__(self, codes, scale, bias=None, clamp: Optional[float] = None):
         _s._setup()

@@ -169,6 +169,18 @@ def _axes(positions, T, sections, dev):
     return _index(positions, axes * T, dev, "positions"), axes, host[1]
 
 
+class _Fixed:
+    """Whose calls pass what its constructor saw, addresses of tensors above all: another value in the place of an attribute
+    of `_fixed` would do nothing, so it is refused.  What the tensors hold may change."""
+
+    _fixed: frozenset = frozenset()
+
+    def __setattr__(self, name, value):
+        if name in self._fixed and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed at construction: make another {type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
 def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                trained: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
     """Cosines and sines of `positions` positions for a rotation over `rot` channels (cl_rope_table): a
@@ -379,7 +391,7 @@ class KVCache:
         return self._work[key]
 
 
-class PagePool:
+class PagePool(_Fixed):
     """Which sequence holds which pages (cl_page_pool), for any caches of one page size on one GPU: block_table int32
     [sequences, width] (a sequence's pages, -1 past the last), lens int32 [sequences] (its tokens), refs int32 [pages] (how
     often a page stands in the table; 0: free) and left_out int32 [1] (sequences that the last `extend` found no room for).
@@ -387,6 +399,8 @@ class PagePool:
     Either sizes are given, and all pages are free, or the three tensors are.  Every operation runs on the GPU in its
     stream's order and can be recorded; the tensors stay where they are.
     """
+
+    _fixed = frozenset(("block_table", "lens", "refs", "left_out", "device", "sequences", "width", "pages", "page_size"))
 
     def __init__(self, pages: int = 0, page_size: int = 64, sequences: int = 1, width: int = 1, device=None,
                  block_table=None, lens=None, refs=None):
