@@ -123,6 +123,11 @@ class Int8Linear(_s._Fixed):
         self._weights = (self.codes.data_ptr(), width, self.scale.data_ptr(),
                          0 if bias is None else self.bias.data_ptr(), N, K)
 
+    def __reduce__(self):
+        # a copy is made anew from the weights: its tensors lie elsewhere
+        own = {k: v for k, v in self.__dict__.items() if k not in self._fixed and k not in ("_clamp", "_width", "_weights")}
+        return type(self), (self.codes[:, :self.K], self.scale, self.bias, self.clamp), own or None
+
     @classmethod
     def from_weight(cls, weight, bias=None, clamp: Optional[float] = None):
         """A layer whose weights [N, K] (float16, bfloat16 or float32) are quantised by output channel."""

@@ -1,5 +1,6 @@
 """Layers and pools hold their tensors' addresses from their construction, so that putting others in their place is refused (no GPU)."""
 import pytest
+import torch
 
 import compressed_linear_amd as cla
 
@@ -36,3 +37,13 @@ def test_a_pool_refuses_other_tensors():
     lens = pool.lens
     pool.lens += [3]  # in place
     assert pool.lens is lens and lens == [1, 2, 3]
+
+
+def test_a_copy_of_a_layer_is_made_from_its_weights():
+    """A deep copy and a pickled layer have tensors of their own, so that the addresses of the first one's must not come along."""
+    codes, scale, bias = torch.zeros(4, 128, dtype=torch.int8), torch.ones(4), torch.ones(4)
+    layer = made(cla.Int8Linear, codes=codes, scale=scale, bias=bias, clamp=2.0, N=4, K=100, device="cuda:0",
+                 _weights=(codes.data_ptr(), 128, scale.data_ptr(), bias.data_ptr(), 4, 100))
+    how, what, *rest = layer.__reduce_ex__(4)
+    assert how is cla.Int8Linear and not any(rest)
+    assert torch.equal(what[0], codes[:, :100]) and what[1] is scale and what[2] is bias and what[3] == 2.0
