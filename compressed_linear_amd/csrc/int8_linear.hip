@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "cl_int8.h"
+#include "int8_plan.h"
 #include "serving.h"
 
 namespace cl {
@@ -12,8 +13,6 @@ constexpr int kMostK = 131071;  // 128 * 128 * K < 2^31
 constexpr int kMostN = 1 << 25;
 constexpr int64_t kMostRow = 1 << 23;  // 256 rows of it are within 32 bits
 constexpr float kLeast = 0x1p-100f;
-
-inline int64_t padded(int64_t K) { return (K + 127) / 128 * 128; }
 
 // A value as it is quantised: clamped where there is a clamp (a NaN stays one).
 __device__ __forceinline__ float clamped(float v, float clamp) { return clamp > 0.f && fabsf(v) > clamp ? copysignf(clamp, v) : v; }
@@ -525,64 +524,7 @@ void launch_quant(const void* x, int dtype, int64_t x_row, int rows, int K, floa
     launch_quant<CL_F32>(x, x_row, rows, K, clamp, codes, row, scale, s);
 }
 
-// ------------------------------------------------------------------- plan
-constexpr int kCus = 256;
-constexpr int kMostParts = 16;
-
-// What int8_stream_kernel takes: up to 16 tokens, and up to 64 with few weights, where reading the tokens once for every 16 outputs costs
-// less than the start of tiles (32 tokens of 4096 x 4096 6.7 us, as tiles 10; 64 8.8 and 10.7; of 4096 x 11008 14.9 and 12.7, of
-// 11008 x 4096 64 18.4 and 16.3).
-bool streamed(int tokens, int N, int K) { return tokens <= 16 || (tokens <= 64 && (int64_t)N * K <= 1 << 25); }
-
-// How a product is cut: the tile, parts of K.
-struct Plan {
-  int shape = 0, parts = 1;
-};
-
-// Tiles, and what they were measured to cost: the microseconds that a step of 128 k takes a CU for each tile that it has, and how
-// many of them run at once.  Few large tiles wait for their loads (256 x 128 with three buffers 1.19 us a step, with two 1.25 where the tile of
-// twice the size takes 1.72); small ones run side by side and fill in for each other, but read more for what they multiply.
-struct Shape {
-  int tw, tt, together;
-  float step;
-};
-constexpr Shape kShapes[] = {{256, 256, 1, 1.72f}, {256, 192, 1, 1.45f}, {256, 128, 1, 1.19f}, {128, 128, 1, 0.54f},
-                             {128, 64, 2, 0.46f},  {64, 64, 2, 0.265f},  {64, 32, 3, 0.235f}};
-constexpr int kShapeCount = sizeof kShapes / sizeof kShapes[0], kHalf = 2;
-
-int64_t tiles_of(const Shape& s, int tokens, int N) { return (((int64_t)tokens + s.tt - 1) / s.tt) * ((N + s.tw - 1) / s.tw); }
-
-// Half of the last round's tiles or fewer: each is cut in two, with a buffer more, so that the round is shorter (2048 x 8192 x 28672 has 3.5
-// rounds: 423 us; with two buffers 452, with whole tiles 459).
-bool halved(int64_t tiles) { return tiles % kCus && tiles % kCus <= kCus / 2; }
-
-// The cheapest of the tiles and parts of K by those costs: steps x tiles of the busiest CU, 3.5 us to fill and to empty each, at least the
-// time to read the weights (8 TB/s is more than memory gives: it ranks the small products), and for parts 4 us and the sums
-// written and read at 4.2 TB/s.  Over 100 products of 24 to 4096 tokens and 1000 x 1000 to 8192 x 28672 weights the choice
-// is 2 % slower than the best of all in the mean, 25 % at worst; 256 x 256 tiles alone would be up to eight times slower.
-Plan plan_product(int tokens, int N, int K) {
-  Plan best;
-  if (tiles_of(kShapes[0], tokens, N) > 4 * kCus) return best;
-  const int steps = (int)(padded(K) / 128);
-  float least = 1e30f;
-  for (int shape = 0; shape < kShapeCount; ++shape) {
-    const Shape& s = kShapes[shape];
-    const int64_t tiles = tiles_of(s, tokens, N);
-    for (int parts = 1; parts <= kMostParts && parts <= (steps + 3) / 4; ++parts) {
-      const int64_t n = tiles * parts;
-      if (parts > 1 && n > 4 * kCus) break;
-      const int each = (steps + parts - 1) / parts;
-      const bool half = shape == 0 && halved(n);
-      const int64_t whole = half ? n / kCus : (n + kCus - 1) / kCus;
-      float t = each * (whole * s.step + (half ? kShapes[kHalf].step : 0)) + 3.5f * ((whole + s.together - 1) / s.together + half);
-      t = std::max(t, (float)N * K / 8e6f);
-      if (parts > 1) t += 4.f + 4.f * tokens * N * parts / 4.2e6f;
-      if (t < least) least = t, best = Plan{shape, parts};
-    }
-  }
-  return best;
-}
-
+// ------------------------------------------------------------------- launches
 size_t sums_bytes(int tokens, int N, int K) {
   if (streamed(tokens, N, K)) return 0;
   const Plan p = plan_product(tokens, N, K);
