@@ -172,8 +172,9 @@ __device__ __forceinline__ void meet() {
 // one barrier of a step stands before its last quarter, whose operands are in registers: behind it the next buffer has arrived
 // everywhere and this one is read by nobody.  Rows past the last and steps past the end are not read (the loads know their buffer's size), and
 // what LDS holds in their place reaches no output.  ONCE: the weights are not kept in the caches, since no other tile reads them.
-// Bound by power and by waiting for memory about equally where there are many tiles (2048 x 8192 x 28672, 411 us, 2.34 POPS: the matrix
-// cores busy 55 % of the time, the clock at 1.9 of 2.4 GHz; with codes of zeros 2.4 GHz), by waiting where there are few.
+// Bound by waiting for memory and, where there are many tiles, by power too (2048 x 8192 x 28672, 417 us, 2.31 POPS launch after launch:
+// the matrix cores busy 60 % of the cycles, the clock at 1.83 of 2.4 GHz; with codes of zeros 367 us, 52 % at 2.41 GHz, so that power costs an
+// eighth and waiting the rest).
 template <int OUT, int TW, int TT, int GW, int GT, int DEPTH, bool ONCE>
 __device__ __forceinline__ void tile(const Product& p, uint8_t* lds, int t0, int n0, int first, int end, int part) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -500,8 +501,8 @@ void launch_quant(const void* x, int64_t x_row, int rows, int K, float clamp, in
   });
 }
 
-// Rows of up to 8192 values are 8 or 16 to a thread, so that as many threads as can be ask for them (2048 rows of 8192 bf16 12.1 us with 512
-// threads, 13.3 with 256, 13.8 with 1024, whose waits for each other cost more; few rows do not care); longer ones 1024 threads' registers up to
+// Rows of up to 8192 values are 8 or 16 to a thread, so that as many threads as can be ask for them (2048 rows of 8192 bf16 12.0 us with 512
+// threads, 13.0 with 256 and with 1024, whose waits for each other cost more; of 4096 7.1 with 256 and 7.0 with 512); longer ones 1024 threads' registers up to
 // 32768.
 template <int IN>
 void launch_quant(const void* x, int64_t x_row, int rows, int K, float clamp, int8_t* codes, int64_t row, float* scale, hipStream_t s) {
@@ -563,8 +564,8 @@ void launch_stream(const Product& p, hipStream_t s) {
 // Tokens past what a launch holds (2^22 tiles of 512 threads) go in pieces, which have tiles enough without parts of K.
 template <int OUT>
 void launch_linear(const Product& p, int K, hipStream_t s) {
-  // eight wavefronts with three buffers: one token of 8192 x 10240 15.4 us, four with three or four 16.5, sixteen 18; with more token rows
-  // two buffers (16 tokens of 8192 x 28672 40.9 us, three 48) and four wavefronts (32 tokens of 4096 x 11008 14.9, eight 17.4)
+  // eight wavefronts with three buffers: one token of 8192 x 10240 15.6 us, four 16.9, with four buffers 16.5, sixteen 18.5; with more
+  // token rows two buffers (16 tokens of 8192 x 28672 41.4 us, three 48.7) and four wavefronts (32 tokens of 4096 x 11008 14.6, eight 17.5)
   if (p.tokens <= 8) return launch_stream<OUT, 8, 3, 8>(p, s);
   if (p.tokens <= 16) return launch_stream<OUT, 8, 2, 16>(p, s);
   if (streamed(p.tokens, p.N, K)) return p.tokens <= 32 ? launch_stream<OUT, 4, 2, 32>(p, s) : launch_stream<OUT, 4, 2, 64>(p, s);

@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(1024) pool_fork_kernel(Pool p, const int32_t* 
 }
 
 // ----------------------------------------------------------------- truncate
-// A wavefront a sequence, since a sequence gives back few pages at a time.  Bound by the launch (1.4 to 3.3 us).
+// A wavefront a sequence, since a sequence mostly gives back few pages at a time.  Bound by the launch then (1.4 to 3 us); a long
+// sequence's end is 64 pages at a time, one load after another (8192 pages 41 us).
 __global__ void __launch_bounds__(64) pool_truncate_kernel(Pool p, const int32_t* __restrict__ to) {
   const int b = blockIdx.x, len = p.lens[b], n = to[b];
   if (n < 0 || n >= len) return;
@@ -334,8 +335,8 @@ __global__ void __launch_bounds__(64) pool_truncate_kernel(Pool p, const int32_t
 // ------------------------------------------------------------------ compact
 // One workgroup.  With n pages held, those from n on move to the free ones below n: the highest to the lowest, up to
 // `most` of them.  Both lists are found by scans, then a thread takes a move at a time.  work[page] is where a moved page went,
-// work[pages] the lowest page that moved.  Bound by the scans and the moves' loads (8.9 us for 2948 moves); the table's new names
-// are a launch of their own, all of its entries side by side (4.8 us).
+// work[pages] the lowest page that moved.  Bound by the scans and the moves' loads (9 us for 2948 moves); the table's new names
+// are a launch of their own, all of its entries side by side (4.7 us).
 __global__ void __launch_bounds__(1024) pool_compact_kernel(Pool p, int most, int32_t* __restrict__ src,
                                                             int32_t* __restrict__ dst, int32_t* __restrict__ work) {
   __shared__ int waves[16];
@@ -388,7 +389,8 @@ __global__ void __launch_bounds__(256) pool_rename_kernel(Pool p, const int32_t*
 
 // --------------------------------------------------------------- copy pages
 // A page of a cache is four runs of bytes (codes and scales of K and V); a workgroup copies one piece of one of them, four loads of 16 bytes
-// under way in a thread.  Bound by memory (2948 pages of 133 KB 152 to 155 us, 5.2 TB/s read and written).
+// under way in a thread.  Bound by memory (2948 pages of 133 KB 141 to 155 us from card to card, 5.2 to 5.7 TB/s read and
+// written).
 struct CopyArgs {
   const int32_t *src, *dst;
   uint8_t* run[4];
@@ -617,7 +619,8 @@ extern "C" cl_status cl_kv_keep(const cl_kv_cache* cache, const int32_t* block_t
     return fail(CL_EINVAL, "keep: a pointer is misaligned");
   if (sequences > 65535) return fail(CL_ESIZE, "keep: more than 65535 sequences");
   const KeepArgs a = {*cache, block_table, ctx_lens, kept, table_width, most, __builtin_ctz(cache->page_size)};
-  // as few threads as have a piece: 64 sequences x 8 heads of 8 drafts 3 us with one wavefront to a workgroup, 6 with four
+  // as few threads as have a piece each, since more only pass through (64 sequences x 8 heads of 8 drafts 3.2 us with 64 threads, 3.3 with
+  // 256); two pieces a thread cost more (16 drafts 3.8 us with 64 threads, 3.3 with 128)
   const int pieces = most * (cache->kind == CL_KV_INT8 ? cache->dim / 16 : cache->dim / 32), threads = std::min(256, (pieces + 63) / 64 * 64);
   const auto kernel = pieces <= 256 ? kv_keep_kernel<1> : pieces <= 512 ? kv_keep_kernel<2> : kv_keep_kernel<8>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)sequences, (unsigned)cache->heads, 2), dim3((unsigned)threads), 0,

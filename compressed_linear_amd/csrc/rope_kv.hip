@@ -437,8 +437,9 @@ void launch_rope(const RopeArgs& a, hipStream_t s) {
     if (!vec) {
       go(rope_pair_kernel<IN, OUT, true>, (int64_t)a.heads * ((a.dim + 1) / 2));
     } else if (many && !wide) {
-      // 8192 x 72 heads of 128, bf16, axes in turn: 50.4 us, as with one axis (48.9); by the kernel of few tokens 71, with four times the
-      // pieces to a workgroup 53.  Wide fp32 heads cover the gathering: 82.4 us by the kernel of few tokens, 86.6 here.
+      // 8192 x 72 heads of 128, bf16, axes in turns: 56.8 us (one axis 54); by the kernel of few tokens 73.5, with two or four tokens to a
+      // workgroup 60.7 and 64.5.  Wide fp32 heads cover the gathering: to bf16 83.2 us by the kernel of few tokens, 85.3 here; to fp32 118
+      // and 114.
       const int each = std::max(1, std::min(kTurnPairs / (a.rot / 2), 512 / (a.heads * (a.dim / 16))));
       in_pieces(a.tokens, 256, [&](int64_t first, int64_t count) {
         hipLaunchKernelGGL((rope_axes_kernel<IN, OUT>), dim3((unsigned)((count + each - 1) / each)), dim3(256), 0, s,

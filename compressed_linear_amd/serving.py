@@ -467,7 +467,8 @@ class PagePool(_Fixed):
     def compact(self, max_moves: Optional[int] = None):
         """Moves the highest pages that are held to the lowest free ones (cl_pool_compact), at most max_moves of them (all
         by default).  Returns (src, dst) int32 [max_moves], -1 past the last: KVCache.copy_pages has to copy them in
-        every cache."""
+        every cache.  An entry that moves nothing still costs those launches a little (12000 pages of 133 KB of which none moves:
+        a list and its copies 50 us by default, 14 with max_moves=256)."""
         dev = self.device
         n = self.pages if max_moves is None else max_moves
         if n < 0:
