@@ -56,8 +56,26 @@ struct RopeArgs {
   const float2* table;
   int64_t x_token, x_head, y_token, y_head;
   int tokens, heads, dim, rot, layout, table_rows;
-  AxisMap axes;  // read with several axes only
 };
+
+// Arguments of a kernel for one axis or for several.  One axis does without the map, whose bytes every launch would carry (a call of
+// cl_rope for one token 3.6 us instead of 3.0).
+template <typename Args>
+struct WithAxes : Args {
+  AxisMap axes;
+};
+template <typename Args, bool AXES>
+using ArgsOf = std::conditional_t<AXES, WithAxes<Args>, Args>;
+static_assert(sizeof(ArgsOf<RopeArgs, false>) + sizeof(AxisMap) <= sizeof(ArgsOf<RopeArgs, true>), "one axis carries no map");
+
+// The address of a token's position, where several axes have one each.
+template <bool AXES, typename Args>
+__device__ __forceinline__ const int32_t* position_at(const Args& a, int axis, int64_t t) {
+  if constexpr (AXES)
+    return a.positions + axis * a.axes.stride + t;
+  else
+    return a.positions + t;
+}
 
 // The axes of pairs 8u to 8u + 7.  Those of 64 pairs are in four words, which a lane picks from sooner than it reads them.
 __device__ __forceinline__ uint32_t axes_of_8(const AxisMap& m, int u) {
@@ -69,7 +87,7 @@ __device__ __forceinline__ int axis_of(const AxisMap& m, int pair) { return m.of
 
 // Any alignment: one thread a pair of channels, rotated or copied.
 template <int IN, int OUT, bool AXES>
-__global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(256) rope_pair_kernel(ArgsOf<RopeArgs, AXES> a) {
   const int pairs = (a.dim + 1) / 2, half = a.rot / 2;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= (int64_t)a.tokens * a.heads * pairs) return;
@@ -85,7 +103,9 @@ __global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
   }
   float u = Elem<IN>::up(x[c1]), v = Elem<IN>::up(x[c2]);
   if (i < half) {
-    const int p = a.positions[AXES ? axis_of(a.axes, i) * a.axes.stride + t : t];
+    int axis = 0;
+    if constexpr (AXES) axis = axis_of(a.axes, i);
+    const int p = *position_at<AXES>(a, axis, t);
     const bool in = p >= 0 && p < a.table_rows;
     const float2 cs = in ? a.table[(int64_t)p * half + i] : make_float2(kNan, kNan);
     rotate_pair(u, v, cs.x, cs.y);
@@ -99,7 +119,7 @@ __global__ void __launch_bounds__(256) rope_pair_kernel(RopeArgs a) {
 // heads but one) once.  Bound by memory, a step by the launch (72 heads of 128, fp32 to bf16: one token 2.4 us, 8192 tokens
 // 81 us, 5.7 TB/s).  With several axes eight pairs of one axis are read as before, others pair by pair.
 template <int IN, int OUT, int HEADS, bool AXES>
-__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(256) rope_kernel(ArgsOf<RopeArgs, AXES> a) {
   const int units = a.dim / 16, half = a.rot / 2, groups = (a.heads + HEADS - 1) / HEADS;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= (int64_t)a.tokens * groups * units) return;
@@ -108,9 +128,10 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   const bool turned = 16 * u < a.rot;
   int c1 = 16 * u, c2 = c1 + 8;
   if (turned && a.layout == CL_ROPE_HALF) c1 = 8 * u, c2 = c1 + half;
-  const uint32_t of = AXES && turned ? axes_of_8(a.axes, u) : 0;
-  const bool one = !AXES || of == (of & 3) * 0x5555;
-  const int p = turned ? a.positions[AXES ? (of & 3) * a.axes.stride + t : t] : 0;
+  uint32_t of = 0;
+  if constexpr (AXES) of = turned ? axes_of_8(a.axes, u) : 0;
+  const bool one = of == (of & 3) * 0x5555;
+  const int p = turned ? *position_at<AXES>(a, of & 3, t) : 0;
   const auto* x = static_cast<const typename Elem<IN>::raw*>(a.x) + t * a.x_token + h * a.x_head;
   auto* y = static_cast<typename Elem<OUT>::raw*>(a.y) + t * a.y_token + h * a.y_head;
   float v1[HEADS][8], v2[HEADS][8];
@@ -122,15 +143,17 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
   }
   if (turned) {
     float2 cs[8];
-    if (AXES && !one) {
-      int on[4];
+    if (!one) {
+      if constexpr (AXES) {
+        int on[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) on[k] = k < a.axes.axes ? a.positions[k * a.axes.stride + t] : 0;
+        for (int k = 0; k < 4; ++k) on[k] = k < a.axes.axes ? *position_at<AXES>(a, k, t) : 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t axis = of >> (2 * i) & 3;
-        const int q = axis & 2 ? (axis & 1 ? on[3] : on[2]) : (axis & 1 ? on[1] : on[0]);
-        cs[i] = q >= 0 && q < a.table_rows ? a.table[(int64_t)q * half + 8 * u + i] : make_float2(kNan, kNan);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t axis = of >> (2 * i) & 3;
+          const int q = axis & 2 ? (axis & 1 ? on[3] : on[2]) : (axis & 1 ? on[1] : on[0]);
+          cs[i] = q >= 0 && q < a.table_rows ? a.table[(int64_t)q * half + 8 * u + i] : make_float2(kNan, kNan);
+        }
       }
     } else if (p >= 0 && p < a.table_rows) {
       const float4* row = reinterpret_cast<const float4*>(a.table + (int64_t)p * half + 8 * u);
@@ -169,12 +192,12 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
 // through their heads in the same pieces.
 constexpr int kTurnPairs = 1024;
 template <int IN, int OUT>
-__global__ void __launch_bounds__(256) rope_axes_kernel(RopeArgs a, int each) {
+__global__ void __launch_bounds__(256) rope_axes_kernel(WithAxes<RopeArgs> a, int each) {
   __shared__ __attribute__((aligned(16))) float2 turn[kTurnPairs];
   const int units = a.dim / 16, half = a.rot / 2, first = blockIdx.x * each, tokens = min(each, a.tokens - first), pieces = a.heads * units;
   for (int i = threadIdx.x; i < tokens * half; i += 256) {
     const int k = i / half, pair = i % half;
-    const int p = a.positions[axis_of(a.axes, pair) * a.axes.stride + first + k];
+    const int p = *position_at<true>(a, axis_of(a.axes, pair), first + k);
     turn[i] = p >= 0 && p < a.table_rows ? a.table[(int64_t)p * half + pair] : make_float2(kNan, kNan);
   }
   __syncthreads();
@@ -215,7 +238,6 @@ struct AppendArgs {
   const int32_t* positions;
   const float2* table;  // NULL: no rotation
   int tokens, rot, layout, table_rows, page_shift, side;
-  AxisMap axes;  // read with several axes only
 };
 
 // Eight channels from `at` of a head at x; VEC: as two 16-byte (fp32) or one load, otherwise one by one.
@@ -246,7 +268,7 @@ __device__ __forceinline__ float lanes_max(float v) {
 // larger part of the bytes and a token's heads lie together there (8192 tokens of 32 fp32 heads of 128, rotated, to int8: 71 us
 // with 16 heads, 80 with 4, 83 with one).  Bound by memory for prompts, by the launch for steps.
 template <int IN, int KIND, int D, bool VEC, bool AXES>
-__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256) kv_append_kernel(ArgsOf<AppendArgs, AXES> a) {
   constexpr int LANES = D / 8;
   const int row_at = threadIdx.x / LANES, h = (blockIdx.y << a.side) + (row_at & ((1 << a.side) - 1)), which = blockIdx.z;
   const int tokens = 256 / LANES >> a.side, first = blockIdx.x * tokens, t = first + (row_at >> a.side);
@@ -259,7 +281,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
       for (int i = threadIdx.x; i < tokens * half; i += 256) {
         const int k = i / half, pair = i % half;
         if (first + k >= a.tokens) break;
-        const int p = a.positions[axis_of(a.axes, pair) * a.axes.stride + first + k];
+        const int p = *position_at<true>(a, axis_of(a.axes, pair), first + k);
         turn[k][pair] = p >= 0 && p < a.table_rows ? a.table[(int64_t)p * half + pair] : make_float2(0.f, 0.f);
       }
       __syncthreads();
@@ -278,7 +300,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
     if constexpr (AXES) {
       cs = turn[row_at >> a.side];
       for (int k = 0; k < a.axes.axes; ++k) {
-        const int p = a.positions[k * a.axes.stride + t];
+        const int p = *position_at<true>(a, k, t);
         in = in && (!(a.axes.used >> k & 1) || (p >= 0 && p < a.table_rows));
       }
     } else {
@@ -415,7 +437,8 @@ __global__ void __launch_bounds__(256) kv_read_kernel(cl_kv_cache c, int page_sh
 int heads_side_by_side(int heads) { return std::min(__builtin_ctz(heads), 4); }
 
 // A launch's part of a call: tokens [first, first + count).
-RopeArgs piece_of(RopeArgs a, int in, int out, int64_t first, int64_t count) {
+template <typename Args>
+Args piece_of(Args a, int in, int out, int64_t first, int64_t count) {
   a.x = beyond(a.x, in, first * a.x_token);
   a.y = beyond(a.y, out, first * a.y_token);
   a.positions += first;
@@ -424,18 +447,19 @@ RopeArgs piece_of(RopeArgs a, int in, int out, int64_t first, int64_t count) {
 }
 
 template <int IN, int OUT>
-void launch_rope(const RopeArgs& a, hipStream_t s) {
+void launch_rope(const WithAxes<RopeArgs>& a, hipStream_t s) {
   const bool vec = a.rot % 16 == 0 && a.dim % 16 == 0 && aligned_to(a.table, 16) &&
                    heads_aligned(a.x, IN, a.x_token, a.x_head) && heads_aligned(a.y, OUT, a.y_token, a.y_head);
-  const auto go = [&](auto kernel, int64_t each) {
+  const auto go = [&](auto kernel, const auto& args, int64_t each) {
     in_pieces(a.tokens, each, [&](int64_t first, int64_t count) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((count * each + 255) / 256)), dim3(256), 0, s, piece_of(a, IN, OUT, first, count));
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((count * each + 255) / 256)), dim3(256), 0, s, piece_of(args, IN, OUT, first, count));
     });
   };
+  const RopeArgs& plain = a;
   if (a.axes.axes > 1) {
     const bool many = (int64_t)a.tokens * a.heads >= (1 << 14), wide = IN == CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17);
     if (!vec) {
-      go(rope_pair_kernel<IN, OUT, true>, (int64_t)a.heads * ((a.dim + 1) / 2));
+      go(rope_pair_kernel<IN, OUT, true>, a, (int64_t)a.heads * ((a.dim + 1) / 2));
     } else if (many && !wide) {
       // 8192 x 72 heads of 128, bf16, axes in turns: 56.8 us (one axis 54); by the kernel of few tokens 73.5, with two or four tokens to a
       // workgroup 60.7 and 64.5.  Wide fp32 heads cover the gathering: to bf16 83.2 us by the kernel of few tokens, 85.3 here; to fp32 118
@@ -446,22 +470,22 @@ void launch_rope(const RopeArgs& a, hipStream_t s) {
                            piece_of(a, IN, OUT, first, count), each);
       });
     } else {
-      go(rope_kernel<IN, OUT, 1, true>, (int64_t)a.heads * (a.dim / 16));
+      go(rope_kernel<IN, OUT, 1, true>, a, (int64_t)a.heads * (a.dim / 16));
     }
     return;
   }
   if (!vec)
-    go(rope_pair_kernel<IN, OUT, false>, (int64_t)a.heads * ((a.dim + 1) / 2));
+    go(rope_pair_kernel<IN, OUT, false>, plain, (int64_t)a.heads * ((a.dim + 1) / 2));
   // Two heads to a thread for many tokens of 16 bits, whose heads are no larger than the cosines and sines (8192 x 72 heads, half
   // of each rotated: 53 us, 55.5 with one and 54 with four; fp32 83 against 81.5; 64 tokens 3.3 against 3.0).
   else if (IN != CL_F32 && (int64_t)a.tokens * a.heads >= (1 << 17))
-    go(rope_kernel<IN, OUT, 2, false>, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
+    go(rope_kernel<IN, OUT, 2, false>, plain, (int64_t)((a.heads + 1) / 2) * (a.dim / 16));
   else
-    go(rope_kernel<IN, OUT, 1, false>, (int64_t)a.heads * (a.dim / 16));
+    go(rope_kernel<IN, OUT, 1, false>, plain, (int64_t)a.heads * (a.dim / 16));
 }
 
 template <int IN>
-void launch_rope(int out, const RopeArgs& a, hipStream_t s) {
+void launch_rope(int out, const WithAxes<RopeArgs>& a, hipStream_t s) {
   if (out == CL_F16)
     launch_rope<IN, CL_F16>(a, s);
   else if (out == CL_BF16)
@@ -470,27 +494,33 @@ void launch_rope(int out, const RopeArgs& a, hipStream_t s) {
     launch_rope<IN, CL_F32>(a, s);
 }
 
-template <int IN, int KIND, int D>
-void launch_append(const AppendArgs& a, hipStream_t s) {
+template <int IN, int KIND, int D, bool AXES>
+void launch_append(const ArgsOf<AppendArgs, AXES>& a, hipStream_t s) {
   const bool vec = heads_aligned(a.src[0], IN, a.token[0], a.head[0]) && heads_aligned(a.src[1], IN, a.token[1], a.head[1]) &&
                    a.rot % 16 == 0;
   const int each = 256 / (D / 8) >> a.side;  // tokens of a workgroup
   in_pieces(a.tokens, (D / 8) << a.side, [&](int64_t first, int64_t count) {
-    AppendArgs b = a;
+    auto b = a;
     for (int w = 0; w < 2; ++w) b.src[w] = beyond(a.src[w], IN, first * a.token[w]);
     b.slots += first;
     if (a.table) b.positions += first;
     b.tokens = (int)count;
     const dim3 grid((unsigned)((count + each - 1) / each), a.c.heads >> a.side, 2);
-    const bool axes = a.table && a.axes.axes > 1;
-    const auto kernel = axes ? (vec ? kv_append_kernel<IN, KIND, D, true, true> : kv_append_kernel<IN, KIND, D, false, true>)
-                             : (vec ? kv_append_kernel<IN, KIND, D, true, false> : kv_append_kernel<IN, KIND, D, false, false>);
+    const auto kernel = vec ? kv_append_kernel<IN, KIND, D, true, AXES> : kv_append_kernel<IN, KIND, D, false, AXES>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, b);
   });
 }
 
+template <int IN, int KIND, int D>
+void launch_append(const WithAxes<AppendArgs>& a, hipStream_t s) {
+  if (a.table && a.axes.axes > 1)
+    launch_append<IN, KIND, D, true>(a, s);
+  else
+    launch_append<IN, KIND, D, false>(a, s);
+}
+
 template <int IN>
-void launch_append(const AppendArgs& a, hipStream_t s) {
+void launch_append(const WithAxes<AppendArgs>& a, hipStream_t s) {
   if (a.c.kind == CL_KV_INT8) {
     if (a.c.dim == 128)
       launch_append<IN, CL_KV_INT8, 128>(a, s);
@@ -576,8 +606,9 @@ namespace {
 
 // The axis of every pair of a rotation over `rot` channels; no sections: one axis.
 cl_status axis_map(const int32_t* sections, int axes, int order, int rot, int tokens, AxisMap* m) {
+  m->axes = 1;
+  if (!sections) return CL_OK;  // nothing else is read
   *m = AxisMap{tokens, 1, 1, {}, {}};
-  if (!sections) return CL_OK;
   if (axes < 1 || axes > 4) return fail(CL_EINVAL, "rope: %d axes (1 to 4 are wanted)", axes);
   if (order != CL_ROPE_BLOCKS && order != CL_ROPE_TURNS) return fail(CL_EINVAL, "rope: unknown order %d of the axes", order);
   const int half = rot / 2;
@@ -634,8 +665,9 @@ extern "C" cl_status cl_rope_axes(const void* x, int32_t x_dtype, int64_t x_toke
   if (y == x && (x_dtype != y_dtype || x_token != y_token || x_head != y_head))
     return fail(CL_EINVAL, "rope: y may be x only with the same type and strides");
   if ((int64_t)tokens * heads >= ((int64_t)1 << 40) / dim) return fail(CL_ESIZE, "rope: tokens * heads * dim at 2^40 or more");
-  RopeArgs a = {x, y, positions, reinterpret_cast<const float2*>(table), x_token, x_head, y_token, y_head,
-                tokens, heads, dim, rot, layout, table_rows, {}};
+  WithAxes<RopeArgs> a;
+  static_cast<RopeArgs&>(a) = {x, y, positions, reinterpret_cast<const float2*>(table), x_token, x_head, y_token, y_head,
+                               tokens, heads, dim, rot, layout, table_rows};
   if ((st = axis_map(sections, axes, order, rot, tokens, &a.axes)) != CL_OK) return st;
   if ((int64_t)heads * ((dim + 1) / 2) > kLaunch) return fail(CL_ESIZE, "rope: too many heads");
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -671,8 +703,9 @@ extern "C" cl_status cl_kv_append_axes(const cl_kv_cache* cache, const void* k, 
   if (!aligned_to(k, elem_size(dtype)) || !aligned_to(v, elem_size(dtype)) || !aligned_to(slots, 4))
     return fail(CL_EINVAL, "append: a pointer is misaligned for its type");
   if (table && (st = check_rope(positions, table, table_rows, rot, layout, cache->dim)) != CL_OK) return st;
-  AppendArgs a = {*cache, {k, v}, {k_token, v_token}, {k_head, v_head}, slots, positions, reinterpret_cast<const float2*>(table),
-                  tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size), heads_side_by_side(cache->heads), {}};
+  WithAxes<AppendArgs> a;
+  static_cast<AppendArgs&>(a) = {*cache, {k, v}, {k_token, v_token}, {k_head, v_head}, slots, positions, reinterpret_cast<const float2*>(table),
+                                 tokens, table ? rot : 0, layout, table_rows, __builtin_ctz(cache->page_size), heads_side_by_side(cache->heads)};
   if (table && (st = axis_map(sections, axes, order, rot, tokens, &a.axes)) != CL_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (dtype == CL_F16)
