@@ -94,7 +94,8 @@ class Int8Linear(_s._Fixed):
 
     codes int8 [N, K] and scale float32 [N] are the weights, by output channel; bias float32 [N]; clamp: the
     activations are clipped to [-clamp, clamp] before they are quantised.  Codes whose K is a multiple of 128 are used as they
-    are; others are copied into rows padded with zeros.
+    are; others are copied into rows padded with zeros.  What a layer was made with stays (its tensors' values may change); a
+    copy, deep or pickled, is a layer of its own.
     """
 
     _fixed = frozenset(("codes", "scale", "bias", "clamp", "N", "K", "device"))
